@@ -1,0 +1,358 @@
+// The cache's blocks: forking sequences, giving blocks up, and compacting the arenas.
+//
+// Records are immutable and found through index entries {offset16, length16}, so a fork
+// copies entries (two entries may name one record) and a free marks them.  Only
+// compaction moves records: out of place, every live record once, in (sequence, head,
+// logical block) order of the first entry that names it.
+//
+// Compaction.  A record is at least 1040 bytes (65 units of 16), and records do not
+// overlap, so at most one starts in any 65 units: owner[offset16 / 65] (atomicMax of the
+// complemented entry number, so the order of arrival does not matter) names the first
+// entry of each record.  One pass of a decoupled look-back over tiles of entries sums
+// the lengths of owned records into new offsets; a second kernel copies the records and
+// writes the new entries.  Bound: HBM, 2 bytes moved per live byte.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace packkv {
+
+namespace {
+
+constexpr uint32_t kFreed = 0xFFFFFFFFu;
+constexpr unsigned long long kFreedEntry = 0xFFFFFFFFull;  // {offset 0xFFFFFFFF, length 0}
+constexpr uint32_t kMinRecord16 = 1040 / 16;
+
+// Index row (in entries) of logical block j of (sequence b, head h), -1 if the block
+// table names no block of the index.
+__device__ __forceinline__ long entry_at(const packkv_cache& c, int b, int h, int j) {
+  long rb = b, jb = j;
+  if (c.block_table != nullptr) {
+    const int p = c.block_table[(size_t)b * c.max_blocks + j];
+    if (p < 0 || (long)p >= (long)c.batch * c.max_blocks) return -1;
+    rb = p / c.max_blocks;
+    jb = p % c.max_blocks;
+  }
+  return (rb * c.kv_heads + h) * c.max_blocks + jb;
+}
+
+__device__ __forceinline__ unsigned long long* entry_ptr(uint32_t* index, long e) {
+  return reinterpret_cast<unsigned long long*>(index) + e;
+}
+
+// Copies n uint4 with the whole CTA.
+__device__ __forceinline__ void copy16(void* dst, const void* src, int n) {
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) d[i] = s[i];
+}
+
+// One CTA per (pair, head): entries, permutations and tail of src's blocks.
+__global__ void __launch_bounds__(256) fork_kernel(const packkv_cache c, const __grid_constant__ PairPlan plan) {
+  const int i = blockIdx.x / c.kv_heads, h = blockIdx.x % c.kv_heads;
+  const int src = plan.src[i], dst = plan.dst[i], nb = plan.blocks[i], tail = plan.tail[i];
+  for (int j = threadIdx.x; j < nb; j += blockDim.x) {
+    const long from = entry_at(c, src, h, j), to = entry_at(c, dst, h, j);
+    if (to < 0) continue;
+    *entry_ptr(c.k_index, to) = from < 0 ? kFreedEntry : *entry_ptr(c.k_index, from);
+    *entry_ptr(c.v_index, to) = from < 0 ? kFreedEntry : *entry_ptr(c.v_index, from);
+  }
+  if (c.perm != nullptr) {
+    for (int x = threadIdx.x; x < nb * 8; x += blockDim.x) {  // 128 bytes of a block: 8 uint4
+      const int j = x >> 3, k = x & 7;
+      const long from = entry_at(c, src, h, j), to = entry_at(c, dst, h, j);
+      if (from < 0 || to < 0) continue;
+      reinterpret_cast<uint4*>(c.perm + to * 128)[k] = reinterpret_cast<const uint4*>(c.perm + from * 128)[k];
+    }
+  }
+  const size_t ts = ((size_t)src * c.kv_heads + h) * 128 * 128, td = ((size_t)dst * c.kv_heads + h) * 128 * 128;
+  copy16(c.k_tail + td, c.k_tail + ts, tail * 16);
+  copy16(c.v_tail + td, c.v_tail + ts, tail * 16);
+}
+
+__global__ void __launch_bounds__(128) free_kernel(const packkv_cache c, const __grid_constant__ RangePlan plan) {
+  const int b = blockIdx.x / c.kv_heads, h = blockIdx.x % c.kv_heads;
+  const int first = plan.first[b], n = plan.count[b];
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    const long e = entry_at(c, b, h, first + j);
+    if (e < 0) continue;
+    *entry_ptr(c.k_index, e) = kFreedEntry;
+    *entry_ptr(c.v_index, e) = kFreedEntry;
+  }
+}
+
+// ---- compaction --------------------------------------------------------------------
+// Workspace: [2][slots] owners, [2][tiles] look-back words, tickets[2], totals[2] (all
+// cleared first), then [2][entries] new offsets.
+constexpr int kTile = 1024;  // entries of a look-back tile, one per thread
+
+struct CompactWs {
+  uint32_t* owner[2];
+  unsigned long long* tile[2];
+  uint32_t* ticket;            // [2]
+  unsigned long long* total;   // [2], written by the last tile
+  uint32_t* moved[2];          // new offset of entry e (owners only)
+  size_t clear_bytes, bytes;
+};
+
+CompactWs compact_ws(void* ws, int64_t entries, uint64_t arena16) {
+  CompactWs w{};
+  uint8_t* p = reinterpret_cast<uint8_t*>(ws);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    uint8_t* r = p + at;
+    at += (n + 15) / 16 * 16;
+    return r;
+  };
+  const size_t slots = arena16 / kMinRecord16 + 1, tiles = (size_t)(entries + kTile - 1) / kTile;
+  for (auto& o : w.owner) o = reinterpret_cast<uint32_t*>(take(slots * 4));
+  for (auto& t : w.tile) t = reinterpret_cast<unsigned long long*>(take(tiles * 8));
+  w.ticket = reinterpret_cast<uint32_t*>(take(8));
+  w.total = reinterpret_cast<unsigned long long*>(take(16));
+  w.clear_bytes = at;
+  for (auto& m : w.moved) m = reinterpret_cast<uint32_t*>(take((size_t)entries * 4));
+  w.bytes = at;
+  return w;
+}
+
+// The entry list of a compaction: entry e is logical block e % most of row e / most.
+struct CompactArgs {
+  packkv_cache dst, src;
+  CompactWs ws;
+  int most;
+  int64_t entries;
+};
+
+// Source entry e of a tensor: false past the sequence's blocks.  *rec = {offset, length},
+// {0xFFFFFFFF, 0} for a freed or an invalid one (*bad).
+__device__ __forceinline__ bool source_entry(const CompactArgs& a, const LengthPlan& plan, int tensor, int64_t e,
+                                             uint2* rec, long* at, bool* bad) {
+  const int row = (int)(e / a.most), j = (int)(e - (int64_t)row * a.most);
+  const int b = row / a.src.kv_heads, h = row - b * a.src.kv_heads;
+  *rec = make_uint2(kFreed, 0u);
+  *bad = false;
+  if (j >= plan.blocks[b]) return false;
+  *at = entry_at(a.src, b, h, j);
+  if (*at < 0) {
+    *bad = true;
+    return true;
+  }
+  const uint2 r = *reinterpret_cast<const uint2*>((tensor ? a.src.v_index : a.src.k_index) + 2 * *at);
+  if (r.x == kFreed) {
+    *bad = r.y != 0u;
+    return true;
+  }
+  const uint32_t most16 = (uint32_t)raw_record_bytes((int)a.src.fmt.bits) / 16u;
+  if (r.y < kMinRecord16 || r.y > most16 || (uint64_t)r.x + r.y > a.src.arena_bytes / 16)
+    *bad = true;
+  else
+    *rec = r;
+  return true;
+}
+
+__global__ void __launch_bounds__(256) mark_kernel(const CompactArgs a, const __grid_constant__ LengthPlan plan) {
+  const int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (x >= 2 * a.entries) return;
+  const int tensor = x >= a.entries;
+  const int64_t e = x - (tensor ? a.entries : 0);
+  uint2 r;
+  long at;
+  bool bad;
+  if (!source_entry(a, plan, tensor, e, &r, &at, &bad) || r.x == kFreed) return;
+  atomicMax(a.ws.owner[tensor] + r.x / kMinRecord16, ~(uint32_t)e);
+}
+
+// Whether entry e, record r, is the first that names its record; *first = that entry,
+// -1 if the slot belongs to a record that overlaps r (a corrupt index).
+__device__ __forceinline__ bool owns_record(const CompactArgs& a, const LengthPlan& plan, int tensor, int64_t e,
+                                            const uint2& r, int64_t* first) {
+  *first = (int64_t)(uint32_t)~a.ws.owner[tensor][r.x / kMinRecord16];
+  if (*first == e) return true;
+  uint2 o;
+  long at;
+  bool bad;
+  source_entry(a, plan, tensor, *first, &o, &at, &bad);
+  if (o.x != r.x || o.y != r.y) *first = -1;
+  return false;
+}
+
+constexpr unsigned long long kAggregate = 1ull << 62, kPrefix = 2ull << 62, kValue = (1ull << 62) - 1;
+
+// Exclusive sums of the owned records' lengths: tile `ticket` of tensor blockIdx.y.
+__global__ void __launch_bounds__(kTile) offsets_kernel(const CompactArgs a, const __grid_constant__ LengthPlan plan) {
+  __shared__ uint32_t warp_sums[kTile / 32];
+  __shared__ uint32_t my_tile;
+  __shared__ unsigned long long before;
+  const int tensor = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) my_tile = atomicAdd(a.ws.ticket + tensor, 1u);  // every earlier tile's CTA has started
+  __syncthreads();
+  const uint32_t tile = my_tile;
+  const int64_t e = (int64_t)tile * kTile + tid;
+  uint32_t len = 0u;
+  if (e < a.entries) {
+    uint2 r;
+    long at;
+    bool bad;
+    int64_t first;
+    if (source_entry(a, plan, tensor, e, &r, &at, &bad) && r.x != kFreed && owns_record(a, plan, tensor, e, r, &first))
+      len = r.y;
+  }
+  uint32_t incl = len;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sums[tid >> 5] = incl;
+  __syncthreads();
+  if (tid < 32) {
+    uint32_t s = warp_sums[tid];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[tid] = s;
+  }
+  __syncthreads();
+  const uint32_t tile_sum = warp_sums[kTile / 32 - 1];
+  if (tid == 0) {
+    unsigned long long* words = a.ws.tile[tensor];
+    unsigned long long sum = 0ull;
+    if (tile > 0) {
+      atomicExch(words + tile, kAggregate | tile_sum);
+      const uint64_t start = global_ns();
+      for (int64_t t = (int64_t)tile - 1; t >= 0;) {
+        const unsigned long long w = atomicAdd(words + t, 0ull);
+        if (w == 0ull) {  // not published yet: bounded wait (an earlier CTA that is running)
+          if (global_ns() - start > 1000000000ull) {
+            set_status(a.dst.ctrl, PACKKV_DEV_TIMEOUT);
+            break;
+          }
+          continue;
+        }
+        sum += w & kValue;
+        if (w & kPrefix) break;
+        --t;
+      }
+    }
+    atomicExch(words + tile, kPrefix | (sum + tile_sum));
+    before = sum;
+    if ((int64_t)(tile + 1) * kTile >= a.entries) a.ws.total[tensor] = sum + tile_sum;
+  }
+  __syncthreads();
+  if (len != 0u)
+    a.ws.moved[tensor][e] = (uint32_t)(before + incl - len + (tid >= 32 ? warp_sums[(tid >> 5) - 1] : 0u));
+}
+
+// Copies: a warp per entry of either tensor (its record if it owns one, the new entry),
+// then a warp per (row, 32 tail tokens) and the permutations.
+__global__ void __launch_bounds__(256) move_kernel(const CompactArgs a, const __grid_constant__ LengthPlan plan) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
+  const int64_t warp0 = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const unsigned long long total_k = a.ws.total[0], total_v = a.ws.total[1];
+  const unsigned long long room = a.dst.arena_bytes / 16;
+  const bool fits = total_k <= room && total_v <= room;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.dst.ctrl[kCtrlKEnd] = fits ? total_k : 0ull;
+    a.dst.ctrl[kCtrlVEnd] = fits ? total_v : 0ull;
+    a.dst.ctrl[kCtrlScratch] = 0ull;
+    if (!fits) set_status(a.dst.ctrl, PACKKV_DEV_CAPACITY);
+  }
+  for (int64_t x = warp0; x < 2 * a.entries; x += warps) {
+    const int tensor = (int)(x & 1);
+    const int64_t e = x >> 1;
+    uint2 r;
+    long at = -1;
+    bool bad;
+    if (!source_entry(a, plan, tensor, e, &r, &at, &bad)) continue;
+    const int row = (int)(e / a.most), j = (int)(e - (int64_t)row * a.most);
+    const int b = row / a.src.kv_heads, h = row - b * a.src.kv_heads;
+    const long to = entry_at(a.dst, b, h, j);
+    unsigned long long entry = kFreedEntry;
+    if (r.x != kFreed && fits) {
+      int64_t first;
+      const bool own = owns_record(a, plan, tensor, e, r, &first);
+      if (first < 0) {
+        bad = true;
+      } else {
+        const uint32_t off = a.ws.moved[tensor][first];
+        if (off + (uint64_t)r.y > room) continue;  // only after a look-back that gave up (status set)
+        entry = (unsigned long long)off | ((unsigned long long)r.y << 32);
+        if (own) {
+          const uint4* s = reinterpret_cast<const uint4*>(tensor ? a.src.v_arena : a.src.k_arena) + r.x;
+          uint4* d = reinterpret_cast<uint4*>(tensor ? a.dst.v_arena : a.dst.k_arena) + off;
+#pragma unroll 4
+          for (uint32_t i = lane; i < r.y; i += 32) __stcs(d + i, __ldcs(s + i));
+        }
+      }
+    }
+    if (bad && lane == 0) set_status(a.dst.ctrl, PACKKV_DEV_BAD_RECORD);
+    if (to < 0) continue;
+    if (lane == 0) *entry_ptr(tensor ? a.dst.v_index : a.dst.k_index, to) = entry;
+    if (tensor == 0 && a.dst.perm != nullptr && at >= 0 && lane < 8)
+      reinterpret_cast<uint4*>(a.dst.perm + to * 128)[lane] =
+          reinterpret_cast<const uint4*>(a.src.perm + at * 128)[lane];
+  }
+  // tails: 32 tokens (512 uint4) per task
+  const int64_t rows = (int64_t)a.src.batch * a.src.kv_heads;
+  for (int64_t x = warp0; x < rows * 8; x += warps) {
+    const int64_t row = x >> 3;
+    const int part = (int)(x & 3);
+    const int tail = plan.tail[row / a.src.kv_heads];
+    const uint16_t* s = (x & 4) ? a.src.v_tail : a.src.k_tail;
+    uint16_t* d = (x & 4) ? a.dst.v_tail : a.dst.k_tail;
+    const uint4* s4 = reinterpret_cast<const uint4*>(s + row * 128 * 128) + part * 512;
+    uint4* d4 = reinterpret_cast<uint4*>(d + row * 128 * 128) + part * 512;
+    const int n = min(512, tail * 16 - part * 512);
+#pragma unroll 4
+    for (int i = lane; i < n; i += 32) d4[i] = s4[i];
+  }
+}
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const packkv_cache& c, const PairPlan& plan, int n, cudaStream_t stream) {
+  fork_kernel<<<(unsigned)(n * c.kv_heads), 256, 0, stream>>>(c, plan);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_free(const packkv_cache& c, const RangePlan& plan, int most, cudaStream_t stream) {
+  const int threads = most >= 128 ? 128 : (most + 31) / 32 * 32;
+  free_kernel<<<(unsigned)(c.batch * c.kv_heads), threads, 0, stream>>>(c, plan);
+  return cudaGetLastError();
+}
+
+size_t compact_workspace_bytes(int64_t entries, uint64_t arena16) { return compact_ws(nullptr, entries, arena16).bytes; }
+
+cudaError_t launch_compact(const packkv_cache& dst, const packkv_cache& src, const LengthPlan& plan, int most, void* ws,
+                           cudaStream_t stream) {
+  CompactArgs a{};
+  a.dst = dst;
+  a.src = src;
+  a.most = most > 0 ? most : 1;
+  a.entries = (int64_t)src.batch * src.kv_heads * a.most;
+  a.ws = compact_ws(ws, a.entries, src.arena_bytes / 16);
+  cudaError_t e = cudaMemsetAsync(ws, 0, a.ws.clear_bytes, stream);
+  if (e != cudaSuccess) return e;
+  mark_kernel<<<(unsigned)((2 * a.entries + 255) / 256), 256, 0, stream>>>(a, plan);
+  offsets_kernel<<<dim3((unsigned)((a.entries + kTile - 1) / kTile), 2), kTile, 0, stream>>>(a, plan);
+  int sms = 148;
+  e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  int64_t grid = (2 * a.entries + 7) / 8;
+  if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
+  move_kernel<<<(unsigned)grid, 256, 0, stream>>>(a, plan);
+  return cudaGetLastError();
+}
+
+}  // namespace packkv

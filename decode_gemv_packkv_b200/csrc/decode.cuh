@@ -347,7 +347,11 @@ __device__ __forceinline__ int i8tab_word(int kap, int kh, int t, int n) {
 // (each the rounding of the remainder so far, so |y - sum| <= 2^-15); digit i goes to
 // column I8Layout<G>::column(head, i), digit 3 and absent heads are zero.  Returns
 // 1/f per head.
-template <int G, int NT>
+// kDigits = 4 fills the otherwise zero fourth column: f is a power of two with 32 <=
+// max|y| < 64 (so y and 1/f are exact), and digits d0 .. d3 leave |y - sum| <= 2^-22,
+// 2^-27 of the largest value instead of 2^-22.  It costs a digit of table building and an
+// FMA per joined row; the products are the same.
+template <int G, int NT, int kDigits = 3>
 __device__ __forceinline__ void build_i8tab(uint32_t* tab, const float (&x)[G][4], float (&invf)[G], int lane) {
   using L = I8Layout<G>;
   static_assert(NT == L::kNT, "n-tiles of the layout");
@@ -357,7 +361,7 @@ __device__ __forceinline__ void build_i8tab(uint32_t* tab, const float (&x)[G][4
   const float2 k128 = make_float2(128.f, 128.f);
 #pragma unroll
   for (int hd = 0; hd < kHeads; ++hd) {
-    uint32_t w0 = 0u, w1 = 0u, w2 = 0u;
+    uint32_t w0 = 0u, w1 = 0u, w2 = 0u, w3 = 0u;
     if (hd < G) {
       const int h = hd < G ? hd : 0;
       const float mx =
@@ -365,10 +369,18 @@ __device__ __forceinline__ void build_i8tab(uint32_t* tab, const float (&x)[G][4
       // |y| <= 127 (the quotient is within 2 ulp); a head whose values are all below
       // 1e-30 gets zero digits (its products are negligible), so f stays finite
       const bool nz = mx > 1e-30f;
-      const float f = nz ? __fdividef(127.f, mx) : 0.f;
-      invf[h] = nz ? __fdividef(mx, 127.f) : 0.f;
+      float f;
+      if constexpr (kDigits == 4) {  // 2^e <= mx < 2^(e+1): f = 2^(5-e)
+        const uint32_t e = __float_as_uint(mx) >> 23;  // biased; mx > 1e-30 is normal, below inf
+        const bool finite = mx < __int_as_float(0x7f800000);
+        f = nz && finite ? __uint_as_float((254u + 5u - e) << 23) : 0.f;
+        invf[h] = nz && finite ? __uint_as_float((e - 5u) << 23) : (nz ? mx : 0.f);
+      } else {
+        f = nz ? __fdividef(127.f, mx) : 0.f;
+        invf[h] = nz ? __fdividef(mx, 127.f) : 0.f;
+      }
       const float2 m128 = make_float2(-128.f, -128.f);
-      float2 t0[2], t1[2], t2[2];
+      float2 t0[2], t1[2], t2[2], rem2[2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const float2 y = __fmul2_rn(make_float2(x[h][2 * q], x[h][2 * q + 1]), make_float2(f, f));
@@ -377,15 +389,23 @@ __device__ __forceinline__ void build_i8tab(uint32_t* tab, const float (&x)[G][4
         t1[q] = __fadd2_rn(r1, R);                                         // low byte: d1 = rint(r1)
         const float2 r2 = __ffma2_rn(__fadd2_rn(t1[q], nR), m128, __fmul2_rn(r1, k128));  // 128(r1 - d1), exact
         t2[q] = __fadd2_rn(r2, R);                                         // low byte: d2 = rint(r2)
+        rem2[q] = r2;
       }
       w0 = pack4(t0[0], t0[1]);
       w1 = pack4(t1[0], t1[1]);
       w2 = pack4(t2[0], t2[1]);
+      if constexpr (kDigits == 4) {
+        float2 t3[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)  // low byte: d3 = rint(128(r2 - d2))
+          t3[q] = __fadd2_rn(__ffma2_rn(__fadd2_rn(t2[q], nR), m128, __fmul2_rn(rem2[q], k128)), R);
+        w3 = pack4(t3[0], t3[1]);
+      }
     }
     tab[i8tab_word<NT>(kap, kh, t, L::column(hd, 0))] = w0;
     tab[i8tab_word<NT>(kap, kh, t, L::column(hd, 1))] = w1;
     tab[i8tab_word<NT>(kap, kh, t, L::column(hd, 2))] = w2;
-    tab[i8tab_word<NT>(kap, kh, t, L::column(hd, 3))] = 0u;
+    tab[i8tab_word<NT>(kap, kh, t, L::column(hd, 3))] = w3;
   }
 }
 
@@ -424,8 +444,11 @@ __device__ __forceinline__ void load_i8frags(const uint32_t* tab, uint32_t (&bf)
 struct PairW {
   float w0, w1, c;
 };
+// (2^-14, 2^-21 with a fourth digit).
+template <int kDigits = 3>
 __device__ __forceinline__ PairW pair_weights(int t) {
-  const float w0 = (t & 1) ? 1.f / 16384.f : 1.f, w1 = (t & 1) ? 0.f : 1.f / 128.f;
+  const float w0 = (t & 1) ? 1.f / 16384.f : 1.f;
+  const float w1 = (t & 1) ? (kDigits == 4 ? 1.f / 2097152.f : 0.f) : 1.f / 128.f;
   return {w0, w1, -(w0 + w1) * kRound};
 }
 
@@ -438,25 +461,29 @@ __device__ __forceinline__ float pair_row(int x0, int x1, const PairW& w) {
 // One row of a split-layout head: digits 0, 1 (x0, x1 of n-tile 2i) and 2 (x2 of
 // n-tile 2i + 1) joined, times the row weight u (a power of two).  The first product
 // cancels all three offsets, so the running value stays below 2^23 * u.
-__device__ __forceinline__ float split_row(int x0, int x1, int x2, float u) {
-  constexpr float c = -kRound * (1.f + 1.f / 128.f + 1.f / 16384.f);  // exact: 16 significant bits
+// A fourth digit (x3, the odd column of n-tile 2i + 1) is chained on in the same way.
+template <int kDigits = 3>
+__device__ __forceinline__ float split_row(int x0, int x1, int x2, int x3, float u) {
+  // exact: 16 significant bits (23 with the fourth digit)
+  constexpr float c = -kRound * (1.f + 1.f / 128.f + 1.f / 16384.f + (kDigits == 4 ? 1.f / 2097152.f : 0.f));
   const float v = fmaf(__int_as_float(x0), u, c * u);
-  return fmaf(__int_as_float(x2), u * (1.f / 16384.f), fmaf(__int_as_float(x1), u * (1.f / 128.f), v));
+  const float r = fmaf(__int_as_float(x2), u * (1.f / 16384.f), fmaf(__int_as_float(x1), u * (1.f / 128.f), v));
+  return kDigits == 4 ? fmaf(__int_as_float(x3), u * (1.f / 2097152.f), r) : r;
 }
 
 // The rows of row tile T for every accumulator set jh: emit(T, jh, lo, hi) with the
 // values of rows g (lo) and g + 8 (hi), digits joined, valid where
 // I8Layout<G>::owns(jh, t).  d: the tile's accumulators over all n-tiles, whose A
 // fields carried the powers of two 1/ug (row g) and 1/uh (row g + 8).
-template <int G, class Emit>
+template <int G, int kDigits = 3, class Emit>
 __device__ __forceinline__ void emit_tile(int T, const int (&d)[I8Layout<G>::kNT][4], float ug, float uh,
                                           const PairW& w, Emit& emit) {
   using L = I8Layout<G>;
   if constexpr (L::kSplit) {
 #pragma unroll
     for (int jh = 0; jh < L::kNH; ++jh)
-      emit(T, jh, split_row(d[2 * jh][0], d[2 * jh][1], d[2 * jh + 1][0], ug),
-           split_row(d[2 * jh][2], d[2 * jh][3], d[2 * jh + 1][2], uh));
+      emit(T, jh, split_row<kDigits>(d[2 * jh][0], d[2 * jh][1], d[2 * jh + 1][0], d[2 * jh + 1][1], ug),
+           split_row<kDigits>(d[2 * jh][2], d[2 * jh][3], d[2 * jh + 1][2], d[2 * jh + 1][3], uh));
   } else {
 #pragma unroll
     for (int j = 0; j < L::kNT; ++j) {
@@ -470,7 +497,7 @@ __device__ __forceinline__ void emit_tile(int T, const int (&d)[I8Layout<G>::kNT
 
 // As emit_tile for a 3-bit record's two planes: bits 0-1 (dl, row weights ulg, ulh) and
 // bit 2 (dh, row weights uhg, uhh, which include the bit's weight 4).
-template <int G, class Emit>
+template <int G, int kDigits = 3, class Emit>
 __device__ __forceinline__ void emit_tile2(int T, const int (&dl)[I8Layout<G>::kNT][4],
                                            const int (&dh)[I8Layout<G>::kNT][4], float ulg, float ulh, float uhg,
                                            float uhh, const PairW& w, Emit& emit) {
@@ -480,8 +507,10 @@ __device__ __forceinline__ void emit_tile2(int T, const int (&dl)[I8Layout<G>::k
     for (int jh = 0; jh < L::kNH; ++jh) {
       const int a = 2 * jh, b = 2 * jh + 1;
       emit(T, jh,
-           split_row(dl[a][0], dl[a][1], dl[b][0], ulg) + split_row(dh[a][0], dh[a][1], dh[b][0], uhg),
-           split_row(dl[a][2], dl[a][3], dl[b][2], ulh) + split_row(dh[a][2], dh[a][3], dh[b][2], uhh));
+           split_row<kDigits>(dl[a][0], dl[a][1], dl[b][0], dl[b][1], ulg) +
+               split_row<kDigits>(dh[a][0], dh[a][1], dh[b][0], dh[b][1], uhg),
+           split_row<kDigits>(dl[a][2], dl[a][3], dl[b][2], dl[b][3], ulh) +
+               split_row<kDigits>(dh[a][2], dh[a][3], dh[b][2], dh[b][3], uhh));
     }
   } else {
 #pragma unroll
@@ -552,12 +581,12 @@ __device__ __forceinline__ void afrag1(uint32_t w0, uint32_t w1, uint32_t (&a)[4
 // accumulator set jh calls emit(T, jh, lo, hi) with the values of rows g (lo) and
 // g + 8 (hi) for head I8Layout<G>::head(jh, t), digits joined (see emit_tile).  Rows
 // are slots (q·Kᵀ, K record) or channels (p·V, V record).
-template <int BITS, int G, bool kWholeBytes, class Emit>
+template <int BITS, int G, bool kWholeBytes, int kDigits = 3, class Emit>
 __device__ __forceinline__ void i8_product(const unsigned char* st,
                                            const uint32_t (&bf)[4][I8Layout<G>::kNT][2], int lane, Emit&& emit) {
   constexpr int NT = I8Layout<G>::kNT;
   const uint4* words = reinterpret_cast<const uint4*>(st + kRawWordOffset);
-  const PairW pw = pair_weights(lane & 3);
+  const PairW pw = pair_weights<kDigits>(lane & 3);
   if constexpr (BITS == 4) {
 #pragma unroll
     for (int T = 0; T < 8; ++T) {
@@ -578,7 +607,7 @@ __device__ __forceinline__ void i8_product(const unsigned char* st,
 #pragma unroll
         for (int j = 0; j < NT; ++j) unmask4(d[j]);
       }
-      emit_tile<G>(T, d, 1.f, 1.f / 16.f, pw, emit);  // low nibbles x1, high nibbles x16
+      emit_tile<G, kDigits>(T, d, 1.f, 1.f / 16.f, pw, emit);  // low nibbles x1, high nibbles x16
     }
   } else if constexpr (BITS == 2) {
 #pragma unroll
@@ -600,8 +629,8 @@ __device__ __forceinline__ void i8_product(const unsigned char* st,
           imma16832(dd[j], ao, bf[kap][j][0], bf[kap][j][1]);
         }
       }
-      emit_tile<G>(2 * P, de, 1.f, 0.25f, pw, emit);               // even tile: x1, x4
-      emit_tile<G>(2 * P + 1, dd, 1.f / 16.f, 1.f / 64.f, pw, emit);  // odd tile: x16, x64
+      emit_tile<G, kDigits>(2 * P, de, 1.f, 0.25f, pw, emit);               // even tile: x1, x4
+      emit_tile<G, kDigits>(2 * P + 1, dd, 1.f / 16.f, 1.f / 64.f, pw, emit);  // odd tile: x16, x64
     }
   } else {
     const uint4* hwords = words + 1024 / 4;  // bit-2 plane
@@ -640,15 +669,15 @@ __device__ __forceinline__ void i8_product(const unsigned char* st,
         }
         // bit 2 weighs 4; tile 4Q + s (s = 2pp, 2pp+1) carries 2^(2s) (row g), 2^(2s+1) (row g+8)
         const float e0 = 4.f / float(1 << (4 * pp)), e1 = 4.f / float(1 << (4 * pp + 2));
-        emit_tile2<G>(2 * P, le, he, 1.f, 0.25f, e0, e0 * 0.5f, pw, emit);
-        emit_tile2<G>(2 * P + 1, lo_, ho, 1.f / 16.f, 1.f / 64.f, e1, e1 * 0.5f, pw, emit);
+        emit_tile2<G, kDigits>(2 * P, le, he, 1.f, 0.25f, e0, e0 * 0.5f, pw, emit);
+        emit_tile2<G, kDigits>(2 * P + 1, lo_, ho, 1.f / 16.f, 1.f / 64.f, e1, e1 * 0.5f, pw, emit);
       }
     }
   }
 }
 
 // q·Kᵀ of one raw K record: scores of all 128 slots for the G heads.
-template <int BITS, int G>
+template <int BITS, int G, int kDigits = 3>
 __device__ __forceinline__ void qk_i8(const unsigned char* st, const uint32_t* tab, const float (&cst)[G],
                                       const float (&invf)[G], float* sblk, long ld, float scale, int lane) {
   using L = I8Layout<G>;
@@ -663,7 +692,7 @@ __device__ __forceinline__ void qk_i8(const unsigned char* st, const uint32_t* t
     sf[jh] = scale * head_sel<G>(invf, head);
     sc[jh] = scale * head_sel<G>(cst, head);
   }
-  i8_product<BITS, G, true>(st, bf, lane, [&](int T, int jh, float lo, float hi) {
+  i8_product<BITS, G, true, kDigits>(st, bf, lane, [&](int T, int jh, float lo, float hi) {
     if (L::owns(jh, t)) {
       float* dst = sblk + L::head(jh, t) * ld + 16 * T + g;
       dst[0] = fmaf(lo, sf[jh], sc[jh]);
@@ -674,7 +703,7 @@ __device__ __forceinline__ void qk_i8(const unsigned char* st, const uint32_t* t
 
 // p·V of one raw V record: adds sum_slots p'*code into the accumulators of channels
 // 16T + g (acc_lo) and 16T + g + 8 (acc_hi) of head I8Layout<G>::head(jh, t).
-template <int BITS, int G>
+template <int BITS, int G, int kDigits = 3>
 __device__ __forceinline__ void pv_i8(const unsigned char* st, const uint32_t* tab, const float (&invf)[G],
                                       float (&acc_lo)[I8Layout<G>::kNH][8], float (&acc_hi)[I8Layout<G>::kNH][8],
                                       int lane) {
@@ -685,7 +714,7 @@ __device__ __forceinline__ void pv_i8(const unsigned char* st, const uint32_t* t
   float f_t[L::kNH];
 #pragma unroll
   for (int jh = 0; jh < L::kNH; ++jh) f_t[jh] = head_sel<G>(invf, L::head(jh, t));
-  i8_product<BITS, G, false>(st, bf, lane, [&](int T, int jh, float lo, float hi) {
+  i8_product<BITS, G, false, kDigits>(st, bf, lane, [&](int T, int jh, float lo, float hi) {
     acc_lo[jh][T] = fmaf(lo, f_t[jh], acc_lo[jh][T]);
     acc_hi[jh][T] = fmaf(hi, f_t[jh], acc_hi[jh][T]);
   });
@@ -872,7 +901,7 @@ __device__ __forceinline__ uint32_t gather4(const uint8_t* t8, const uint4 d, in
 // 4*lane .. +3; cst: sum_c q_c mn_c per head.  Writes the 128 scores of every head:
 // scale * (cst + sum_c q'_c base_gc + sum_c q'_c offset).
 // Returns false (nothing written) if the record fails the prologue's checks.
-template <int BITS, int G>
+template <int BITS, int G, int kDigits = 3>
 __device__ __forceinline__ bool qk_packed_tc(unsigned char* st, uint32_t len, const uint32_t* tab,
                                              const float (&qv)[G][4], const float (&cst)[G], const float (&invf)[G],
                                              float* sblk, long ld, float scale, int lane) {
@@ -903,7 +932,7 @@ __device__ __forceinline__ bool qk_packed_tc(unsigned char* st, uint32_t len, co
       part = warp_sum(part);
       if (lane == 0) bsm[g * G + hd] = part + cst[hd];
     }
-  const PairW pw = pair_weights(t);
+  const PairW pw = pair_weights<kDigits>(t);
   float sf[L::kNH];
 #pragma unroll
   for (int jh = 0; jh < L::kNH; ++jh) sf[jh] = scale * head_sel<G>(invf, L::head(jh, t));
@@ -958,7 +987,7 @@ __device__ __forceinline__ bool qk_packed_tc(unsigned char* st, uint32_t len, co
           *reinterpret_cast<float2*>(dst) = make_float2(fmaf(lo, sf[jh], sc_[jh]), fmaf(hi, sf[jh], sc_[jh]));
         }
       };
-      emit_tile<G>(u, acc[u], 1.f, 1.f, pw, emit);
+      emit_tile<G, kDigits>(u, acc[u], 1.f, 1.f, pw, emit);
     }
   }
   return true;
@@ -1067,7 +1096,7 @@ __device__ __forceinline__ void pv_nat_unit(const uint32_t* words, int gs, uint3
 // sum_r p'_r code[r][c], digits joined and times invf, into sacc (the warp's [G][128]
 // channel sums).  tab: the int8 B table of p' in natural slot order (build_i8tab).
 // Returns false (nothing added) if the record fails the prologue's checks.
-template <int BITS, int G>
+template <int BITS, int G, int kDigits = 3>
 __device__ __forceinline__ bool pv_packed_nat(unsigned char* st, uint32_t len, const uint32_t* tab,
                                               const float (&invf)[G], float* sacc, int lane) {
   using L = I8Layout<G>;
@@ -1114,7 +1143,7 @@ __device__ __forceinline__ bool pv_packed_nat(unsigned char* st, uint32_t len, c
   __syncwarp();  // descriptors written
   const uint32_t* words = reinterpret_cast<const uint32_t*>(st + kPackedWordOffset);
   const uint32_t* dsc = reinterpret_cast<const uint32_t*>(st) + g8;
-  const PairW pw = pair_weights(t);
+  const PairW pw = pair_weights<kDigits>(t);
   float f_t[L::kNH];
 #pragma unroll
   for (int jh = 0; jh < L::kNH; ++jh) f_t[jh] = head_sel<G>(invf, L::head(jh, t));
@@ -1145,7 +1174,7 @@ __device__ __forceinline__ bool pv_packed_nat(unsigned char* st, uint32_t len, c
         row[8] = fmaf(hi, f_t[jh], row[8]);
       }
     };
-    emit_tile<G>(T, d, 1.f, 1.f, pw, emit);
+    emit_tile<G, kDigits>(T, d, 1.f, 1.f, pw, emit);
   }
   __syncwarp();  // sums added before other lanes read or add them
   return true;

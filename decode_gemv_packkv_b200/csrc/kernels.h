@@ -115,4 +115,78 @@ struct AttnArgs {
 cudaError_t launch_attention(AttnArgs a, const RaggedPlan* plan, cudaStream_t stream);
 size_t attention_workspace_bytes(int batch, int kv_heads, int group);
 
+// Norm and rotation of query and key heads, values cast beside them (rope.cu).
+struct HeadsTensor {
+  const void* data;  // NULL: absent
+  int64_t batch_stride, token_stride, head_stride;  // elements
+  int heads;
+  const float* weight;  // [128] or NULL
+  uint16_t* out;        // [batch][heads][tokens][128]; appends: k and v tails [batch][heads][128][128]
+};
+struct HeadsArgs {
+  HeadsTensor x[3];  // q, k, v
+  int dtype;         // PACKKV_DTYPE_*
+  int batch, tokens;
+  bool norm;
+  float eps;
+  const int32_t* positions;  // [batch][tokens] or NULL (first + t)
+  int64_t first;
+  packkv_rope rope;
+};
+// Tokens each sequence of a ragged batch holds (0xFFFFFFFF: it takes no token).
+struct RaggedLengths {
+  uint32_t tokens[kMaxRaggedBatch];
+};
+cudaError_t launch_prompt_heads(const HeadsArgs& a, cudaStream_t stream);
+// `tokens` held by every sequence, or the lengths of a ragged batch.
+cudaError_t launch_append_heads(const HeadsArgs& a, uint32_t tokens, const RaggedLengths* lengths,
+                                cudaStream_t stream);
+
+// The blocks of a cache (blocks.cu).  Per-sequence arguments travel by value.
+struct PairPlan {  // sequence dst[i] becomes src[i], which holds blocks[i] blocks and tail[i] tail tokens
+  int16_t src[kMaxRaggedBatch], dst[kMaxRaggedBatch];
+  int32_t blocks[kMaxRaggedBatch];
+  uint8_t tail[kMaxRaggedBatch];
+};
+struct RangePlan {  // logical blocks [first, first + count) of every sequence
+  int32_t first[kMaxRaggedBatch], count[kMaxRaggedBatch];
+};
+struct LengthPlan {  // what every sequence holds
+  int32_t blocks[kMaxRaggedBatch];
+  uint8_t tail[kMaxRaggedBatch];
+};
+cudaError_t launch_fork(const packkv_cache& c, const PairPlan& plan, int n, cudaStream_t stream);
+cudaError_t launch_free(const packkv_cache& c, const RangePlan& plan, int most, cudaStream_t stream);
+size_t compact_workspace_bytes(int64_t entries, uint64_t arena16);
+// most: blocks of the longest sequence
+cudaError_t launch_compact(const packkv_cache& dst, const packkv_cache& src, const LengthPlan& plan, int most, void* ws,
+                           cudaStream_t stream);
+
+// Decode attention with a sliding window and first tokens that stay visible (window.cu).
+struct WindowArgs {
+  const uint8_t* k_arena;
+  const uint8_t* v_arena;
+  const uint32_t* k_index;
+  const uint32_t* v_index;
+  const uint16_t* k_tail;
+  const uint16_t* v_tail;
+  const uint8_t* perm;      // NULL: slot = token
+  const int32_t* block_table;
+  uint64_t* ctrl;
+  uint64_t arena16;
+  int batch, kv_heads, max_blocks, bits;
+  int rows;                 // query rows per kv head: queries * group
+  int group, queries, window, sinks;
+  int n_blocks, tail_len;   // uniform batches
+  int most_items;           // items of the longest row (seen blocks, pieces of the tail)
+  const uint16_t* q;        // [batch][kv_heads][rows][128]
+  float scale;
+  float* out;
+  float* partials;
+};
+size_t window_workspace_bytes(int batch, int kv_heads, int rows);
+// Items of a row with nb blocks and tl tail tokens (window.cu's item list).
+int window_items(const WindowArgs& a, int nb, int tl);
+cudaError_t launch_window(const WindowArgs& a, const LengthPlan* plan, cudaStream_t stream);
+
 }  // namespace packkv

@@ -1,0 +1,338 @@
+// Norm of the query and key heads with the position rotation in the same pass, values
+// cast beside them, and the single-token form that appends to the cache's tails.
+//
+// Per head of 128 channels, fp32: y_c = x_c * rsqrt(mean x^2 + eps) * w_c, then each
+// rotated pair (a, b) -> amplitude * (a cos t - b sin t, b cos t + a sin t), one rounding
+// to fp16.  The angle of pair i at a position is position * turn[i] in 2^-64 turns, a
+// wrapping 64-bit product: exact modulo whole turns however far the position, so the
+// fp32 sine and cosine see an argument in [-1, 1) half turns that is off by 2^-25.
+//
+// Bound: HBM bytes (each input and output element once; about 10 instructions per
+// element).  A CTA takes a few tokens of one sequence and all their heads, so that one
+// sine and cosine per (token, pair) in shared memory serve every head.  A half-warp
+// takes one head; lane l has channels A..A+3 and B..B+3, chosen so that both members of
+// each pair sit in one lane (no shuffles for the rotation): half layout A = 4l,
+// B = rot/2 + 4l (the unrotated rest packed behind), interleaved A = 4l, B = 64 + 4l.
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace packkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokTile = 4;                  // tokens of a CTA: one sine and cosine per thread
+constexpr int kRowSlots = kThreads / 16;     // heads in flight per CTA
+
+template <class T>
+struct Vec4;  // four consecutive elements
+template <>
+struct Vec4<__half> {
+  using Raw = uint2;
+  __device__ static float4 widen(const uint2& r) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+};
+template <>
+struct Vec4<__nv_bfloat16> {
+  using Raw = uint2;
+  __device__ static float4 widen(const uint2& r) {
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xFFFF0000u));
+  }
+};
+template <>
+struct Vec4<float> {
+  using Raw = uint4;
+  __device__ static float4 widen(const uint4& r) {
+    return make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
+  }
+};
+
+__device__ __forceinline__ float widen1(__half x) { return __half2float(x); }
+__device__ __forceinline__ float widen1(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float widen1(float x) { return x; }
+
+__device__ __forceinline__ uint2 half4(const float (&y)[4]) {
+  const __half2 a = __floats2half2_rn(y[0], y[1]), b = __floats2half2_rn(y[2], y[3]);
+  uint2 r;
+  r.x = *reinterpret_cast<const uint32_t*>(&a);
+  r.y = *reinterpret_cast<const uint32_t*>(&b);
+  return r;
+}
+
+// The channels of a lane and how its pairs turn.  Wide (vector accesses): ca + i and
+// cb + i, i < 4.  Narrow (half layouts whose rot_dim is no multiple of 8, and unaligned
+// rows): element i at channels ca_i and cb_i.
+struct LaneMap {
+  int ca[4], cb[4];
+  int pa[4], pb[4];  // pair of element i of A and of B
+};
+
+// Layout of lane l (0..15).  half: (A_i, B_i) is pair pa[i]; interleaved: (A_0, A_1),
+// (A_2, A_3), (B_0, B_1), (B_2, B_3) are pairs.
+template <bool kHalf, bool kWide>
+__device__ __forceinline__ LaneMap lane_map(int rot, int l) {
+  LaneMap m;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (!kHalf) {
+      m.ca[i] = 4 * l + i;
+      m.cb[i] = 64 + 4 * l + i;
+      m.pa[i] = 2 * l + (i >> 1);
+      m.pb[i] = 32 + 2 * l + (i >> 1);
+    } else if constexpr (kWide) {  // rot a multiple of 8
+      const bool turned = 8 * l < rot;
+      m.ca[i] = (turned ? 4 * l : rot + 8 * (l - rot / 8)) + i;
+      m.cb[i] = (turned ? rot / 2 + 4 * l : rot + 8 * (l - rot / 8) + 4) + i;
+      m.pa[i] = m.pb[i] = 4 * l + i;
+    } else {
+      const int p = l + 16 * i;  // pair p < rot/2, or the (p - rot/2)-th two unrotated channels
+      const bool turned = 2 * p < rot;
+      m.ca[i] = turned ? p : 2 * p;
+      m.cb[i] = turned ? p + rot / 2 : 2 * p + 1;
+      m.pa[i] = m.pb[i] = p;
+    }
+  }
+  return m;
+}
+
+struct HeadRow {
+  float a[4], b[4];
+};
+
+template <class T, bool kWide>
+struct RowLoad {  // the loads of a row, before the conversion
+  typename Vec4<T>::Raw ra, rb;
+  __device__ void issue(const T* p, const LaneMap& m) {
+    ra = __ldcs(reinterpret_cast<const typename Vec4<T>::Raw*>(p + m.ca[0]));
+    rb = __ldcs(reinterpret_cast<const typename Vec4<T>::Raw*>(p + m.cb[0]));
+  }
+  __device__ HeadRow get() const {
+    const float4 x = Vec4<T>::widen(ra), y = Vec4<T>::widen(rb);
+    return {{x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}};
+  }
+};
+template <class T>
+struct RowLoad<T, false> {
+  T ra[4], rb[4];
+  __device__ void issue(const T* p, const LaneMap& m) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ra[i] = p[m.ca[i]];
+      rb[i] = p[m.cb[i]];
+    }
+  }
+  __device__ HeadRow get() const {
+    HeadRow r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.a[i] = widen1(ra[i]);
+      r.b[i] = widen1(rb[i]);
+    }
+    return r;
+  }
+};
+
+template <bool kHalf, bool kWide>
+__device__ __forceinline__ void store_row(uint16_t* dst, const HeadRow& r, const LaneMap& m) {
+  if constexpr (kWide || !kHalf) {  // channels ca[0]..+3, cb[0]..+3; outputs are 16-byte aligned
+    *reinterpret_cast<uint2*>(dst + m.ca[0]) = half4(r.a);
+    *reinterpret_cast<uint2*>(dst + m.cb[0]) = half4(r.b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dst[m.ca[i]] = __half_as_ushort(__float2half_rn(r.a[i]));
+      dst[m.cb[i]] = __half_as_ushort(__float2half_rn(r.b[i]));
+    }
+  }
+}
+
+// Norm (w = this lane's weights) and rotation of one row; cs = the row's token's table.
+template <bool kHalf>
+__device__ __forceinline__ void turn_row(HeadRow& r, bool norm, float eps, const HeadRow& w, const float2* cs,
+                                         const LaneMap& m, int rot) {
+  if (norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss = fmaf(r.a[i], r.a[i], fmaf(r.b[i], r.b[i], ss));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);  // within the half-warp
+    const float f = rsqrtf(fmaf(ss, 1.f / 128.f, eps));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.a[i] *= f * w.a[i];
+      r.b[i] *= f * w.b[i];
+    }
+  }
+  // pairs from rot/2 on are left untouched (not multiplied by 1 and 0: an infinity
+  // would spoil its neighbour)
+  if constexpr (kHalf) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (2 * m.pa[i] < rot) {
+        const float2 z = cs[m.pa[i]];
+        const float a = r.a[i], b = r.b[i];
+        r.a[i] = a * z.x - b * z.y;
+        r.b[i] = b * z.x + a * z.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      if (2 * m.pa[i] < rot) {
+        const float2 z = cs[m.pa[i]];
+        const float a = r.a[i], b = r.a[i + 1];
+        r.a[i] = a * z.x - b * z.y;
+        r.a[i + 1] = b * z.x + a * z.y;
+      }
+      if (2 * m.pb[i] < rot) {
+        const float2 z = cs[m.pb[i]];
+        const float a = r.b[i], b = r.b[i + 1];
+        r.b[i] = a * z.x - b * z.y;
+        r.b[i + 1] = b * z.x + a * z.y;
+      }
+    }
+  }
+}
+
+// Where a token goes.  Prompts: token t of sequence b at positions[b*T + t] (or first +
+// t), outputs [b][head][t].  Appends: one token per sequence at the length the plan (or
+// the uniform length) gives, k and v at that slot of the tails.
+struct PromptPlan {};
+
+template <class Plan>
+constexpr bool is_append = !std::is_same<Plan, PromptPlan>::value;
+
+struct UniformLength {
+  uint32_t tokens;
+};
+
+// Tokens sequence b holds (kNoToken: it takes none).
+constexpr uint32_t kNoToken = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t length_of(const UniformLength& p, int) { return p.tokens; }
+__device__ __forceinline__ uint32_t length_of(const RaggedLengths& p, int b) { return p.tokens[b]; }
+
+template <class T, bool kHalf, bool kWide, class Plan>
+__global__ void __launch_bounds__(kThreads) heads_kernel(const HeadsArgs a, const __grid_constant__ Plan plan) {
+  __shared__ float2 table[kTokTile][64];
+  const int tiles = is_append<Plan> ? 1 : (a.tokens + kTokTile - 1) / kTokTile;
+  const int b = blockIdx.x / tiles;
+  const int t0 = (blockIdx.x - b * tiles) * kTokTile;
+  const int nt = is_append<Plan> ? 1 : min(kTokTile, a.tokens - t0);
+  const int rot = (int)a.rope.rot_dim;
+  uint32_t held = 0;
+  if constexpr (is_append<Plan>) {
+    held = length_of(plan, b);
+    if (held == kNoToken) return;
+  }
+  for (int i = threadIdx.x; i < nt * 64; i += kThreads) {
+    const int p = i & 63, t = i >> 6;
+    if (2 * p < rot) {
+      long long pos;
+      if constexpr (is_append<Plan>)
+        pos = held;
+      else
+        pos = a.positions ? (long long)a.positions[(size_t)b * a.tokens + t0 + t] : a.first + t0 + t;
+      // signed turns in [-1/2, 1/2) as 64-bit fractions -> half turns
+      const long long turns = (long long)((unsigned long long)pos * a.rope.turn[p]);
+      float s, c;
+      sincospif((float)turns * 1.0842021724855044e-19f, &s, &c);  // 2^-63
+      table[t][p] = make_float2(c * a.rope.amplitude, s * a.rope.amplitude);
+    }
+  }
+  const int l = threadIdx.x & 15;
+  const LaneMap m = lane_map<kHalf, kWide>(rot, l);
+  __syncthreads();
+  const int slot = threadIdx.x >> 4;
+#pragma unroll 1
+  for (int which = 0; which < 3; ++which) {  // q, k, v
+    const HeadsTensor& x = a.x[which];
+    if (x.data == nullptr) continue;
+    const T* src = reinterpret_cast<const T*>(x.data) + b * x.batch_stride;
+    const bool norm = a.norm && which < 2;
+    HeadRow w = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}};
+    if (norm && x.weight != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w.a[i] = x.weight[m.ca[i]];
+        w.b[i] = x.weight[m.cb[i]];
+      }
+    }
+    const int rows = nt * x.heads;
+    // whole warps stay in the loop (the norm's shuffles); a row past the end repeats the last
+    for (int r0 = 0; r0 < rows; r0 += kRowSlots) {
+      const int r = min(r0 + slot, rows - 1);
+      const int t = r / x.heads, h = r - t * x.heads;
+      RowLoad<T, kWide> in;
+      in.issue(src + (t0 + t) * x.token_stride + h * x.head_stride, m);
+      HeadRow y = in.get();
+      if (which < 2) turn_row<kHalf>(y, norm, a.eps, w, table[t], m, rot);
+      if (r0 + slot < rows) {
+        size_t at;
+        if (!is_append<Plan> || which == 0)
+          at = ((size_t)b * x.heads + h) * a.tokens + t0 + t;
+        else
+          at = ((size_t)b * x.heads + h) * kBlockTokens + (held & (kBlockTokens - 1));
+        store_row<kHalf, kWide>(x.out + at * kHeadDim, y, m);
+      }
+    }
+  }
+}
+
+template <class T, bool kHalf, bool kWide, class Plan>
+cudaError_t launch_heads_t(const HeadsArgs& a, const Plan& plan, cudaStream_t stream) {
+  const long tiles = is_append<Plan> ? 1 : (a.tokens + (long)kTokTile - 1) / kTokTile;
+  heads_kernel<T, kHalf, kWide, Plan><<<(unsigned)(tiles * a.batch), kThreads, 0, stream>>>(a, plan);
+  return cudaGetLastError();
+}
+
+// Vector accesses need four consecutive elements aligned to their size everywhere.
+bool wide_ok(const HeadsArgs& a) {
+  const int bytes = a.dtype == PACKKV_DTYPE_FP32 ? 16 : 8;
+  if (a.rope.layout == PACKKV_ROPE_HALF && a.rope.rot_dim % 8 != 0) return false;
+  for (const HeadsTensor& x : a.x) {
+    if (x.data == nullptr) continue;
+    if (reinterpret_cast<uintptr_t>(x.data) % bytes != 0) return false;
+    if (x.batch_stride % 4 != 0 || x.token_stride % 4 != 0 || x.head_stride % 4 != 0) return false;
+  }
+  return true;
+}
+
+template <class T, class Plan>
+cudaError_t launch_heads_d(const HeadsArgs& a, const Plan& plan, cudaStream_t stream) {
+  const bool half = a.rope.layout == PACKKV_ROPE_HALF;
+  if (wide_ok(a))
+    return half ? launch_heads_t<T, true, true, Plan>(a, plan, stream)
+                : launch_heads_t<T, false, true, Plan>(a, plan, stream);
+  return half ? launch_heads_t<T, true, false, Plan>(a, plan, stream)
+              : launch_heads_t<T, false, false, Plan>(a, plan, stream);
+}
+
+template <class Plan>
+cudaError_t launch_heads_p(const HeadsArgs& a, const Plan& plan, cudaStream_t stream) {
+  if (a.dtype == PACKKV_DTYPE_FP16) return launch_heads_d<__half, Plan>(a, plan, stream);
+  if (a.dtype == PACKKV_DTYPE_BF16) return launch_heads_d<__nv_bfloat16, Plan>(a, plan, stream);
+  return launch_heads_d<float, Plan>(a, plan, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_heads(const HeadsArgs& a, cudaStream_t stream) {
+  return launch_heads_p(a, PromptPlan{}, stream);
+}
+
+cudaError_t launch_append_heads(const HeadsArgs& a, uint32_t tokens, const RaggedLengths* lengths,
+                                cudaStream_t stream) {
+  if (lengths != nullptr) return launch_heads_p(a, *lengths, stream);
+  return launch_heads_p(a, UniformLength{tokens}, stream);
+}
+
+}  // namespace packkv

@@ -1,0 +1,625 @@
+// Decode attention over the packed cache with a sliding window and first tokens that
+// stay visible (sinks), for one or several query positions per sequence.
+//
+//   out[r] = sum_i w_i v_i,  w = softmax over the visible i of scale * q[r]·k_i
+//   query s at p = T - queries + s sees i <= p with i > p - window or i < sinks.
+//
+// Items of a (sequence, kv head) row: the blocks that hold first tokens, the blocks from
+// the first query's window on, and the tail in pieces of 32 tokens.  A block that every
+// query sees whole needs no mask; any other is masked slot by slot through the block's
+// permutation.  Records go through the int8 tensor-core decode of the other products
+// (decode.cuh), the fp16 tail through m16n8k16 (q·k exact products, p as two halves).
+// The running maximum and sum of the softmax, and the value sums, are fp32.
+//
+// A cluster of CTAs serves one row (up to 8 query rows of it): its warps take the items
+// in turn, each with its K and V record in flight together, and the warps' sums are
+// merged through (distributed) shared memory in a fixed order, so the call is one launch
+// and its results do not depend on timing.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+#include <unordered_map>
+
+#include "decode.cuh"
+
+namespace packkv {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kWinWarps = 4;
+constexpr int kTailPiece = 32;
+// Four digits of q' and p' (decode.cuh): over a long window the values average out, and
+// three digits' score error (2^-22 of the largest q') showed as 1.7e-5 of the output.
+constexpr int kWinDigits = 4;
+constexpr float kWinLog2e = 1.4426950408889634f;
+constexpr float kMinusInf = -__builtin_huge_valf();
+
+template <int BITS, int G>
+struct WinCfg {
+  using C = Cfg<BITS, G, false>;
+  static constexpr int kNT = C::kNT;
+  static constexpr int kStage = C::kStageRec;
+  static constexpr int kTableBytes = (C::kI8Tab + 15) / 16 * 16;
+  static constexpr int kScoreBytes = 512 * G;
+  static constexpr int kSumBytes = 512 * G;
+  static constexpr int kFixed = 2 * kStage + kTableBytes + kScoreBytes + kSumBytes;
+  static constexpr int kWarpSmem = (kFixed + 32 + 127) / 128 * 128;
+};
+
+// Warp-private shared memory: [K stage][V stage][table][scores][sums][2 mbarriers][2 kinds].
+template <int BITS, int G>
+struct WinMem {
+  using W = WinCfg<BITS, G>;
+  unsigned char* base;
+  __device__ unsigned char* stage(int s) const { return base + s * W::kStage; }
+  __device__ uint32_t* table() const { return reinterpret_cast<uint32_t*>(base + 2 * W::kStage); }
+  __device__ float* scores() const { return reinterpret_cast<float*>(base + 2 * W::kStage + W::kTableBytes); }
+  __device__ float* sums() const { return scores() + 128 * G; }
+  __device__ uint64_t* bar(int s) const { return reinterpret_cast<uint64_t*>(base + W::kFixed) + s; }
+  __device__ int* kind(int s) const { return reinterpret_cast<int*>(base + W::kFixed + 16) + s; }
+};
+
+// The items of a row that holds nb blocks and tl tail tokens.
+struct ItemList {
+  int front;  // blocks [0, front) hold first tokens
+  int from;   // then blocks [from, nb)
+  int nb, tl;
+  int n;      // items in all
+};
+
+__host__ __device__ inline ItemList item_list(int queries, int window, int sinks, int nb, int tl) {
+  ItemList x;
+  x.nb = nb;
+  x.tl = tl;
+  const long long first = (long long)nb * 128 + tl - queries - (long long)window + 1;  // oldest token a window holds
+  const long long s = ((long long)sinks + 127) / 128;
+  x.front = (int)(s < nb ? s : nb);
+  x.from = first > 0 ? (int)(first / 128) : 0;
+  if (x.from < x.front) x.from = x.front;
+  if (x.from > nb) x.from = nb;
+  x.n = x.front + (nb - x.from) + (tl + kTailPiece - 1) / kTailPiece;
+  return x;
+}
+
+__device__ __forceinline__ int row_blocks(const WindowArgs& a, const NoPlan&, int) { return a.n_blocks; }
+__device__ __forceinline__ int row_blocks(const WindowArgs&, const LengthPlan& p, int b) { return p.blocks[b]; }
+__device__ __forceinline__ int row_tail(const WindowArgs& a, const NoPlan&, int) { return a.tail_len; }
+__device__ __forceinline__ int row_tail(const WindowArgs&, const LengthPlan& p, int b) { return p.tail[b]; }
+
+// What one query row sees, relative to a block's first token.
+__device__ __forceinline__ bool sees(long long pos, long long p, int window, int sinks) {
+  return pos <= p && (pos > p - window || pos < sinks);
+}
+
+// m16n8k16, fp16 operands, fp32 accumulators.
+__device__ __forceinline__ void hmma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Scaled scores of n <= 32 tail tokens (rows of 128 fp16 from `tail`) into sc[head*128 + t].
+// The contraction's channel order is free: lane (g, t) takes channels 32 kk + 8t .. +7 of
+// its token (A) and of its head (B) with one 16-byte load each, two k-steps per load.
+template <int G>
+__device__ __forceinline__ void tail_piece_scores(const uint16_t* tail, const uint16_t* q, int n, float scale,
+                                                  float* sc, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 qb[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+    qb[kk] = g < G ? *reinterpret_cast<const uint4*>(q + (size_t)g * 128 + 32 * kk + 8 * t) : zero;
+#pragma unroll
+  for (int tile = 0; tile < 2; ++tile) {
+    if (16 * tile >= n) break;
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    const int r0 = 16 * tile + g, r1 = r0 + 8;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const uint4 x = r0 < n ? *reinterpret_cast<const uint4*>(tail + (size_t)r0 * 128 + 32 * kk + 8 * t) : zero;
+      const uint4 y = r1 < n ? *reinterpret_cast<const uint4*>(tail + (size_t)r1 * 128 + 32 * kk + 8 * t) : zero;
+      hmma16816(d, x.x, y.x, x.y, y.y, qb[kk].x, qb[kk].y);
+      hmma16816(d, x.z, y.z, x.w, y.w, qb[kk].z, qb[kk].w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int head = 2 * t + (i & 1), tok = (i & 2) ? r1 : r0;
+      if (head < G) sc[head * 128 + tok] = scale * d[i];
+    }
+  }
+}
+
+// Adds sum_t p[head][t] v[t][c] of n <= 32 tail tokens into the channel sums (p: fp32 in
+// sc[head*128 + t], zero from n to 31).  p = hi + lo/4096 with fp16 hi, lo (abs. error
+// below 2^-35): rows g of the A tile carry hi, rows g + 8 lo, so one product sums both.
+// Column n of n-tile j is channel 16n + j: lane (g, t) reads 16 channels of its tokens.
+// With an infinity or NaN among the values the tokens are added one by one, those of zero
+// weight left out.
+template <int G>
+__device__ __forceinline__ void tail_piece_values(const uint16_t* tail, const float* sc, int n, float* sacc,
+                                                  int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  float d[16][4];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+  uint32_t wild = 0u;
+#pragma unroll
+  for (int tile = 0; tile < 2; ++tile) {
+    if (16 * tile >= n) break;
+    uint32_t a[4];  // rows g (hi): k 2t, 2t+1 | rows g + 8 (lo) | k + 8
+#pragma unroll
+    for (int kh = 0; kh < 2; ++kh) {
+      const int k = 16 * tile + 2 * t + 8 * kh;
+      const float p0 = g < G ? sc[g * 128 + k] : 0.f, p1 = g < G ? sc[g * 128 + k + 1] : 0.f;
+      const __half2 hi = __floats2half2_rn(p0, p1);
+      const float2 hf = __half22float2(hi);
+      const __half2 lo = __floats2half2_rn((p0 - hf.x) * 4096.f, (p1 - hf.y) * 4096.f);
+      a[2 * kh] = *reinterpret_cast<const uint32_t*>(&hi);
+      a[2 * kh + 1] = *reinterpret_cast<const uint32_t*>(&lo);
+    }
+    uint4 v[4][2];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the tile, channels 16g .. 16g+15
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = 16 * tile + 2 * t + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        v[i][x] = tok < n ? *reinterpret_cast<const uint4*>(tail + (size_t)tok * 128 + 16 * g + 8 * x)
+                          : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {v[i][x].x, v[i][x].y, v[i][x].z, v[i][x].w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {  // an exponent of all ones in either half
+          wild |= ((w[y] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4& q4 = v[i][j >> 3];
+        const int word = (j >> 1) & 3;
+        w[i] = word == 0 ? q4.x : (word == 1 ? q4.y : (word == 2 ? q4.z : q4.w));
+      }
+      const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+      hmma16816(d[j], a[0], a[1], a[2], a[3], __byte_perm(w[0], w[1], sel), __byte_perm(w[2], w[3], sel));
+    }
+  }
+  if (__any_sync(0xffffffffu, wild != 0u)) {
+#pragma unroll 1
+    for (int hd = 0; hd < G; ++hd)
+#pragma unroll 1
+      for (int sl = 0; sl < 4; ++sl) {
+        float s = 0.f;
+        for (int tok = 0; tok < n; ++tok) {
+          const float p = sc[hd * 128 + tok];
+          if (p != 0.f) s = fmaf(p, half_bits_to_float(tail[(size_t)tok * 128 + sl * 32 + lane]), s);
+        }
+        sacc[hd * 128 + sl * 32 + lane] += s;
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)  // rows g: columns 2t, 2t + 1; their lo parts sit in rows g + 8
+        if (g < G) sacc[g * 128 + 16 * (2 * t + i) + j] += fmaf(d[j][2 + i], 1.f / 4096.f, d[j][i]);
+  }
+  __syncwarp();
+}
+
+// The four parameters of this lane (channels or slots 4*lane ..) at `at` of a record.
+__device__ __forceinline__ float4 param4(const unsigned char* st, int at, int lane) {
+  const uint2 v = *reinterpret_cast<const uint2*>(st + at + 8 * lane);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+  return make_float4(x.x, x.y, y.x, y.y);
+}
+
+// Scores of a staged K record into sc; false: the record failed its checks.
+template <int BITS, int G>
+__device__ __forceinline__ bool record_scores(unsigned char* st, int kind_len, uint32_t* tab, const float (&qr)[G][4],
+                                              float* sc, float scale, int lane) {
+  constexpr int NT = WinCfg<BITS, G>::kNT;
+  const float4 mn = param4(st, kParamOffset, lane), sl = param4(st, kParamOffset + 256, lane);
+  float cst[G], qv[G][4], invf[G];
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) {
+    cst[hd] = warp_sum(fmaf(qr[hd][3], mn.w, fmaf(qr[hd][2], mn.z, fmaf(qr[hd][1], mn.y, qr[hd][0] * mn.x))));
+    qv[hd][0] = qr[hd][0] * sl.x;
+    qv[hd][1] = qr[hd][1] * sl.y;
+    qv[hd][2] = qr[hd][2] * sl.z;
+    qv[hd][3] = qr[hd][3] * sl.w;
+  }
+  build_i8tab<G, NT, kWinDigits>(tab, qv, invf, lane);
+  __syncwarp();
+  if ((kind_len & 0xFF) == kKindRaw) {
+    qk_i8<BITS, G, kWinDigits>(st, tab, cst, invf, sc, 128, scale, lane);
+    return true;
+  }
+  return qk_packed_tc<BITS, G, kWinDigits>(st, (uint32_t)(kind_len >> 8) * 16u, tab, qv, cst, invf, sc, 128, scale, lane);
+}
+
+// Adds the staged V record's values weighted by pr (slots 4*lane + i) into the accumulators
+// (raw) or the channel sums (compressed) and the min terms; false: failed its checks.
+template <int BITS, int G>
+__device__ __forceinline__ bool record_values(unsigned char* st, int kind_len, uint32_t* tab, const float (&pr)[G][4],
+                                              float (&acc_lo)[I8Layout<G>::kNH][8],
+                                              float (&acc_hi)[I8Layout<G>::kNH][8], float* sacc, float (&mp)[G],
+                                              int lane) {
+  constexpr int NT = WinCfg<BITS, G>::kNT;
+  const float4 mn = param4(st, kParamOffset, lane), sl = param4(st, kParamOffset + 256, lane);
+  float pv[G][4], add[G], invf[G];
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) {
+    add[hd] = fmaf(pr[hd][3], mn.w, fmaf(pr[hd][2], mn.z, fmaf(pr[hd][1], mn.y, pr[hd][0] * mn.x)));
+    pv[hd][0] = pr[hd][0] * sl.x;
+    pv[hd][1] = pr[hd][1] * sl.y;
+    pv[hd][2] = pr[hd][2] * sl.z;
+    pv[hd][3] = pr[hd][3] * sl.w;
+  }
+  build_i8tab<G, NT, kWinDigits>(tab, pv, invf, lane);
+  __syncwarp();
+  if ((kind_len & 0xFF) == kKindRaw)
+    pv_i8<BITS, G, kWinDigits>(st, tab, invf, acc_lo, acc_hi, lane);
+  else if (!pv_packed_nat<BITS, G, kWinDigits>(st, (uint32_t)(kind_len >> 8) * 16u, tab, invf, sacc, lane))
+    return false;
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) mp[hd] += add[hd];
+  return true;
+}
+
+template <int BITS, int G, class Plan>
+__global__ void __launch_bounds__(kWinWarps * 32) window_kernel(const WindowArgs a,
+                                                                const __grid_constant__ Plan plan) {
+  using W = WinCfg<BITS, G>;
+  using L = I8Layout<G>;
+  constexpr int NH = L::kNH;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float wmax[kWinWarps][G], wsum[kWinWarps][G], cmax[G], csum[G];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunks = a.rows / G;
+  const int rc = blockIdx.x / ranks;
+  const int bh = rc / chunks, chunk = rc - bh * chunks;
+  const int b = bh / a.kv_heads, h = bh - b * a.kv_heads;
+  const WinMem<BITS, G> m{smem + warp * W::kWarpSmem};
+  const ItemList items = item_list(a.queries, a.window, a.sinks, row_blocks(a, plan, b), row_tail(a, plan, b));
+  const long long T = (long long)items.nb * 128 + items.tl;
+  const long long p0 = T - a.queries;  // position of query 0
+  if (lane == 0) {
+    mbar_init(m.bar(0), 1);
+    mbar_init(m.bar(1), 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  // block of item i (>= nb: piece i's tail tokens)
+  auto block_of = [&](int i) { return i < items.front ? i : items.from + (i - items.front); };
+  // issues the K (s = 0) or V (s = 1) record of block j into stage s
+  auto issue = [&](int s, int j) {
+    uint32_t off = 0xFFFFFFFFu, len = 0u;
+    int kind = kKindTail;
+    if (j < items.nb) {
+      size_t at = (size_t)bh * a.max_blocks + j;
+      bool there = true;
+      if (a.block_table != nullptr) {
+        const int p = a.block_table[(size_t)b * a.max_blocks + j];
+        there = p >= 0 && (long)p < (long)a.batch * a.max_blocks;
+        at = there ? ((size_t)(p / a.max_blocks) * a.kv_heads + h) * a.max_blocks + p % a.max_blocks : 0;
+      }
+      if (there) {
+        const uint2 e = *reinterpret_cast<const uint2*>((s ? a.v_index : a.k_index) + at * 2);
+        off = e.x;
+        len = e.y;
+      }
+      const bool valid = off != 0xFFFFFFFFu && len >= 1040 / 16 && len * 16u <= (uint32_t)W::kStage &&
+                         (uint64_t)off + len <= a.arena16;
+      kind = !valid ? kKindInvalid : (len * 16u == (uint32_t)W::kStage ? kKindRaw : kKindPacked);
+    }
+    if (lane == 0) {
+      *m.kind(s) = kind | (int)(len << 8);
+      fence_async_smem();
+      if (kind == kKindRaw || kind == kKindPacked) {
+        mbar_arrive_expect_tx(m.bar(s), len * 16u);
+        bulk_g2s(m.stage(s), (s ? a.v_arena : a.k_arena) + (uint64_t)off * 16, len * 16u, m.bar(s));
+      } else {
+        mbar_arrive(m.bar(s));
+      }
+    }
+    __syncwarp();
+  };
+
+  const int step = ranks * kWinWarps;
+  const int first = rank * kWinWarps + warp;
+  if (first < items.n) {
+    issue(0, block_of(first));
+    issue(1, block_of(first));
+  }
+  const uint16_t* qrow = a.q + ((size_t)bh * a.rows + (size_t)chunk * G) * 128;
+  float qr[G][4], mrun[G], lrun[G], mp[G];
+  float acc_lo[NH][8], acc_hi[NH][8];
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) {
+    const uint2 v = *reinterpret_cast<const uint2*>(qrow + hd * 128 + 4 * lane);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+    qr[hd][0] = x.x;
+    qr[hd][1] = x.y;
+    qr[hd][2] = y.x;
+    qr[hd][3] = y.y;
+    mrun[hd] = kMinusInf;
+    lrun[hd] = 0.f;
+    mp[hd] = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NH; ++j)
+#pragma unroll
+    for (int T8 = 0; T8 < 8; ++T8) acc_lo[j][T8] = acc_hi[j][T8] = 0.f;
+  float* sacc = m.sums();
+  float* sc = m.scores();
+  zero_sums<G>(sacc, lane);
+  __syncwarp();
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t phase = 0u;
+#pragma unroll 1
+  for (int i = first; i < items.n; i += step, phase ^= 1u) {
+    const int j = block_of(i);
+    const bool more = i + step < items.n;
+    // ---- scores ----
+    if (!mbar_wait_bounded(m.bar(0), phase, a.ctrl)) {  // never landed (status set)
+      mbar_wait_bounded(m.bar(1), phase, a.ctrl);
+      break;
+    }
+    const int kind_k = *m.kind(0);
+    const bool tail = (kind_k & 0xFF) == kKindTail;
+    const int piece = tail ? j - items.nb : 0;
+    const int n_tok = tail ? min(kTailPiece, items.tl - piece * kTailPiece) : 128;
+    const size_t tail_at = ((size_t)bh * 128 + piece * kTailPiece) * 128;
+    bool ok = true;
+    if (tail)
+      tail_piece_scores<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
+    else if ((kind_k & 0xFF) == kKindInvalid)
+      ok = false;
+    else
+      ok = record_scores<BITS, G>(m.stage(0), kind_k, m.table(), qr, sc, a.scale, lane);
+    __syncwarp();
+    if (more) issue(0, block_of(i + step));
+
+    // ---- masks and the running softmax ----
+    const long long pos0 = (long long)j * 128;
+    const bool whole = !tail && pos0 + 127 <= p0 && (pos0 > p0 + a.queries - 1 - a.window || pos0 + 127 < a.sinks);
+    long long pos[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) pos[x] = pos0 + 4 * lane + x;
+    if (tail) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) pos[x] = (long long)items.nb * 128 + piece * kTailPiece + 4 * lane + x;
+    } else if (!whole && a.perm != nullptr) {
+      size_t at = (size_t)bh * a.max_blocks + j;
+      bool there = true;
+      if (a.block_table != nullptr) {
+        const int p = a.block_table[(size_t)b * a.max_blocks + j];
+        there = p >= 0 && (long)p < (long)a.batch * a.max_blocks;
+        at = there ? ((size_t)(p / a.max_blocks) * a.kv_heads + h) * a.max_blocks + p % a.max_blocks : 0;
+      }
+      const uint32_t w = there ? reinterpret_cast<const uint32_t*>(a.perm + at * 128)[lane] : 0u;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) pos[x] = pos0 + ((w >> (8 * x)) & 0xFFu);
+    }
+    float pr[G][4];
+#pragma unroll
+    for (int hd = 0; hd < G; ++hd) {
+      const long long p = p0 + (chunk * G + hd) / a.group;
+      float sv[4];
+      float bm = kMinusInf;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int r = 4 * lane + x;
+        const bool see = ok && r < n_tok && (whole || sees(pos[x], p, a.window, a.sinks));
+        sv[x] = see ? sc[hd * 128 + r] : kMinusInf;
+        bm = fmaxf(bm, sv[x]);
+      }
+      bm = warp_max(bm);
+      const float m_new = fmaxf(mrun[hd], bm);
+      float ps = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        pr[hd][x] = sv[x] == kMinusInf ? 0.f : exp2f((sv[x] - m_new) * kWinLog2e);
+        ps += pr[hd][x];
+      }
+      ps = warp_sum(ps);
+      if (m_new > mrun[hd]) {  // warp-uniform: rescale what was summed under the old maximum
+        const float alpha = mrun[hd] == kMinusInf ? 0.f : exp2f((mrun[hd] - m_new) * kWinLog2e);
+        lrun[hd] *= alpha;
+        mp[hd] *= alpha;
+#pragma unroll
+        for (int sl = 0; sl < 4; ++sl) sacc[hd * 128 + sl * 32 + lane] *= alpha;
+#pragma unroll
+        for (int jn = 0; jn < NH; ++jn) {
+          if (L::head(jn, t) == hd) {
+#pragma unroll
+            for (int T8 = 0; T8 < 8; ++T8) {
+              acc_lo[jn][T8] *= alpha;
+              acc_hi[jn][T8] *= alpha;
+            }
+          }
+        }
+        mrun[hd] = m_new;
+      }
+      lrun[hd] += ps;
+    }
+
+    // ---- values ----
+    if (!mbar_wait_bounded(m.bar(1), phase, a.ctrl)) {
+      if (more) mbar_wait_bounded(m.bar(0), phase ^ 1u, a.ctrl);
+      break;
+    }
+    const int kind_v = *m.kind(1);
+    if (tail) {
+      __syncwarp();
+#pragma unroll
+      for (int hd = 0; hd < G; ++hd)
+        *reinterpret_cast<float4*>(sc + hd * 128 + 4 * lane) = make_float4(pr[hd][0], pr[hd][1], pr[hd][2], pr[hd][3]);
+      __syncwarp();
+      tail_piece_values<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
+    } else if ((kind_v & 0xFF) == kKindInvalid) {
+      ok = false;
+    } else if (ok) {
+      ok = record_values<BITS, G>(m.stage(1), kind_v, m.table(), pr, acc_lo, acc_hi, sacc, mp, lane);
+    }
+    if (!ok && lane == 0) set_status(a.ctrl, PACKKV_DEV_BAD_RECORD);
+    __syncwarp();
+    if (more) issue(1, block_of(i + step));
+  }
+
+  // ---- this warp's sums, then the CTA's, then the cluster's, each in a fixed order ----
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < NH; ++j) {
+    if (L::owns(j, t)) {
+      float* row = sacc + L::head(j, t) * 128 + g;
+#pragma unroll
+      for (int T8 = 0; T8 < 8; ++T8) {
+        row[16 * T8] += acc_lo[j][T8];
+        row[16 * T8 + 8] += acc_hi[j][T8];
+      }
+    }
+  }
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) {
+    const float mn = warp_sum(mp[hd]);
+    __syncwarp();
+#pragma unroll
+    for (int sl = 0; sl < 4; ++sl) sacc[hd * 128 + sl * 32 + lane] += mn;
+    if (lane == 0) {
+      wmax[warp][hd] = mrun[hd];
+      wsum[warp][hd] = lrun[hd];
+    }
+  }
+  __syncthreads();
+  const WinMem<BITS, G> m0{smem};
+  float* cta = m0.scores();  // [G][128], free now
+  for (int o = threadIdx.x; o < G * 128; o += kWinWarps * 32) {
+    const int hd = o >> 7;
+    float M = wmax[0][hd];
+#pragma unroll
+    for (int w = 1; w < kWinWarps; ++w) M = fmaxf(M, wmax[w][hd]);
+    float s = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWinWarps; ++w) {
+      const WinMem<BITS, G> mw{smem + w * W::kWarpSmem};
+      const float e = wsum[w][hd] == 0.f ? 0.f : exp2f((wmax[w][hd] - M) * kWinLog2e);
+      if (e != 0.f) s = fmaf(mw.sums()[o], e, s);
+      l = fmaf(wsum[w][hd], e, l);
+    }
+    cta[o] = s;
+    if ((o & 127) == 0) {
+      cmax[hd] = M;
+      csum[hd] = l;
+    }
+  }
+  if (ranks > 1) cluster.sync(); else __syncthreads();
+  float* orow = a.out + ((size_t)bh * a.rows + (size_t)chunk * G) * 128;
+  for (int o = rank * kWinWarps * 32 + threadIdx.x; o < G * 128; o += ranks * kWinWarps * 32) {
+    const int hd = o >> 7;
+    float M = kMinusInf;
+    for (int r = 0; r < ranks; ++r) M = fmaxf(M, *cluster.map_shared_rank(&cmax[hd], r));
+    float s = 0.f, l = 0.f;
+    for (int r = 0; r < ranks; ++r) {
+      const float lr = *cluster.map_shared_rank(&csum[hd], r);
+      const float e = lr == 0.f ? 0.f : exp2f((*cluster.map_shared_rank(&cmax[hd], r) - M) * kWinLog2e);
+      if (e != 0.f) s = fmaf(*cluster.map_shared_rank(&cta[o], r), e, s);
+      l = fmaf(lr, e, l);
+    }
+    orow[o] = l == 0.f ? 0.f : s / l;  // a row that sees nothing is zero; a NaN stays one
+  }
+  if (ranks > 1) cluster.sync();  // no CTA leaves while another reads its sums
+}
+
+struct WinKernel {
+  const void* fn;
+  int smem;
+};
+
+template <class Plan>
+bool win_select(int bits, int g, WinKernel* k) {
+#define PACKKV_WCASE(B, GG)                                                                                     \
+  if (bits == B && g == GG) {                                                                                   \
+    *k = {reinterpret_cast<const void*>(&window_kernel<B, GG, Plan>), kWinWarps * WinCfg<B, GG>::kWarpSmem};     \
+    return true;                                                                                                \
+  }
+  PACKKV_WCASE(4, 1) PACKKV_WCASE(4, 2) PACKKV_WCASE(4, 4) PACKKV_WCASE(4, 8)
+  PACKKV_WCASE(3, 1) PACKKV_WCASE(3, 2) PACKKV_WCASE(3, 4) PACKKV_WCASE(3, 8)
+  PACKKV_WCASE(2, 1) PACKKV_WCASE(2, 2) PACKKV_WCASE(2, 4) PACKKV_WCASE(2, 8)
+#undef PACKKV_WCASE
+  return false;
+}
+
+// Raises the kernel's shared memory limit once per device and reads the SM count.
+cudaError_t win_configure(const WinKernel& k, int* sms) {
+  static std::mutex mu;
+  static std::unordered_map<long long, int> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const long long key = (long long)(reinterpret_cast<uintptr_t>(k.fn)) * 64 + dev;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = done.find(key);
+  if (it != done.end()) {
+    *sms = it->second;
+    return cudaSuccess;
+  }
+  e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  done[key] = *sms;
+  return cudaSuccess;
+}
+
+template <class Plan>
+cudaError_t launch_window_t(const WindowArgs& a, const Plan& plan, cudaStream_t stream) {
+  const int g = a.rows < 8 ? a.rows : 8;
+  WinKernel k{};
+  if (!win_select<Plan>(a.bits, g, &k)) return cudaErrorInvalidValue;
+  int sms = 0;
+  cudaError_t e = win_configure(k, &sms);
+  if (e != cudaSuccess) return e;
+  const long row_chunks = (long)a.batch * a.kv_heads * (a.rows / g);
+  int ranks = 1;
+  while (ranks < 8 && ranks * kWinWarps < a.most_items && row_chunks * ranks * 2 <= 2L * sms) ranks *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(row_chunks * ranks));
+  cfg.blockDim = dim3(kWinWarps * 32);
+  cfg.dynamicSmemBytes = (size_t)k.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  WindowArgs copy = a;
+  void* args[] = {&copy, const_cast<Plan*>(&plan)};
+  return cudaLaunchKernelExC(&cfg, k.fn, args);
+}
+
+}  // namespace
+
+int window_items(const WindowArgs& a, int nb, int tl) { return item_list(a.queries, a.window, a.sinks, nb, tl).n; }
+
+size_t window_workspace_bytes(int, int, int) { return 0; }
+
+cudaError_t launch_window(const WindowArgs& a, const LengthPlan* plan, cudaStream_t stream) {
+  return plan ? launch_window_t<LengthPlan>(a, *plan, stream) : launch_window_t<NoPlan>(a, NoPlan{}, stream);
+}
+
+}  // namespace packkv

@@ -274,6 +274,167 @@ size_t packkv_attention_workspace_bytes(const packkv_cache* cache, int32_t q_hea
 packkv_status packkv_attention_decode(const packkv_cache* cache, const uint16_t* q, int32_t q_heads,
                                       float scale, float* out, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * ---- Preparing the heads: norm and position rotation --------------------------------
+ * What a decoder layer does to its query and key heads before they meet the cache
+ * (the PackKV pages start behind it, at the cached K and V).  In fp32, rounded to fp16
+ * once at the end:
+ *   y_c  = x_c * rsqrt(mean_c x_c^2 + eps) * w_c           (if eps >= 0, else y = x)
+ *   pairs (a, b) of the first rot_dim channels:
+ *   (a, b) -> amplitude * (a cos t - b sin t, b cos t + a sin t),  t = position * frequency
+ * Channels from rot_dim on pass unrotated (and without the amplitude).
+ */
+#define PACKKV_DTYPE_FP16 0
+#define PACKKV_DTYPE_BF16 1
+#define PACKKV_DTYPE_FP32 2
+
+#define PACKKV_ROPE_HALF 0u         /* pair i = channels (i, i + rot_dim/2) */
+#define PACKKV_ROPE_INTERLEAVED 1u  /* pair i = channels (2i, 2i + 1) */
+
+/* How the frequencies f_i = theta^(-2i/rot_dim) are scaled for contexts longer than the
+ * trained ones: LINEAR f/factor; BASE theta * factor^(rot_dim/(rot_dim-2)) in theta's
+ * place (rot_dim > 2); PARTS k f + (1-k) f/factor with k = clamp((n - low)/(high - low), 0, 1)
+ * and n = original_tokens * f / 2pi, the turns a pair makes within the trained length. */
+#define PACKKV_ROPE_SCALE_NONE 0
+#define PACKKV_ROPE_SCALE_LINEAR 1
+#define PACKKV_ROPE_SCALE_BASE 2
+#define PACKKV_ROPE_SCALE_PARTS 3
+
+/* A rotation, as packkv_rope_init lays it down.  turn[i] is pair i's frequency as a
+ * fraction of a turn per position, times 2^64: position * turn[i] (mod 2^64) is the
+ * angle to within position * 2^-65 turns, however far the position. */
+typedef struct {
+  uint32_t layout;    /* PACKKV_ROPE_HALF / _INTERLEAVED */
+  uint32_t rot_dim;   /* rotated channels: even, 0..128 */
+  float amplitude;    /* factor on cos and sin */
+  uint32_t reserved0;
+  uint64_t turn[64];
+} packkv_rope;
+
+/* Fills *rope.  PACKKV_ERR_INVALID_ARG (and *rope unchanged) for an odd or too large
+ * rot_dim, an unknown layout or scaling, theta <= 1, factor <= 0, a non-finite amplitude,
+ * and for PARTS original_tokens <= 0 or high <= low.  Frequencies that do not lie in
+ * (0, pi] per position are refused too. */
+packkv_status packkv_rope_init(packkv_rope* rope, uint32_t rot_dim, uint32_t layout, double theta,
+                               int32_t scaling, double factor, double original_tokens, double low,
+                               double high, float amplitude);
+
+/* Heads of 128 channels as a projection leaves them: element (b, t, h, c) of a tensor is
+ * data[b*batch_stride + t*token_stride + h*head_stride + c] (strides in elements, any
+ * sign; head_stride 128 and token_stride (q_heads + 2*kv_heads)*128 for one fused
+ * projection).  data: device, aligned to its element; 16-byte aligned data and strides
+ * take the wide loads. */
+typedef struct {
+  const void* data;
+  int64_t batch_stride, token_stride, head_stride;
+} packkv_rows;
+
+typedef struct {
+  int32_t dtype;      /* PACKKV_DTYPE_*, of q, k and v */
+  int32_t q_heads;    /* 0: no q (q.data NULL) */
+  int32_t kv_heads;
+  float eps;          /* of the norm; negative: no norm */
+  packkv_rows q, k, v;    /* k and v: both or neither (NULL data) for packkv_norm_rope */
+  const float* q_weight;  /* device fp32 [128] (4-byte aligned) or NULL (ones); without a norm NULL */
+  const float* k_weight;
+} packkv_heads;
+
+/*
+ * Norm and rotation of q and k, v cast, from token-major rows to the layouts the cache
+ * calls take: q_out, k_out, v_out device fp16 [batch][heads][tokens][128] (k_out and
+ * v_out feed packkv_encode_block).  rope NULL: no rotation.  The position of token t of
+ * sequence b is positions[b*tokens + t] (device int32, any order, negative ones turn
+ * back) or, with positions NULL, first + t.  Values beyond the fp16 range become
+ * infinities.  Outputs must not overlap the inputs.  batch or tokens 0 is a no-op.
+ */
+packkv_status packkv_norm_rope(const packkv_rope* rope, const packkv_heads* in, int32_t batch, int32_t tokens,
+                               const int32_t* positions, int64_t first, uint16_t* q_out, uint16_t* k_out,
+                               uint16_t* v_out, void* stream);
+
+/*
+ * One new token per sequence, prepared and appended in one launch: as packkv_norm_rope
+ * for in's single token (token_stride is not used; in->kv_heads = cache->kv_heads), at
+ * the position the cache gives it (the tokens its sequence holds before the call), with
+ * k and v written to the cache's tails and q to q_out (device fp16 [batch][q_heads][128],
+ * the q of the attention calls).  Then as packkv_append_token: tails that reach 128
+ * tokens are encoded, the counters advance.  active (host uint8 [batch], ragged caches
+ * only) selects the sequences as in packkv_append_token_masked; NULL: all.  q_out rows
+ * of sequences that take no token are left as they were.
+ */
+packkv_status packkv_append_norm_rope(packkv_cache* cache, const packkv_rope* rope, const packkv_heads* in,
+                                      const uint8_t* active, uint16_t* q_out, void* stream);
+
+/*
+ * Decode attention over the packed cache with a sliding window and first tokens that
+ * stay visible.  `queries` query positions per sequence, the last ones the cache holds
+ * (their k and v are appended before the call): query s of sequence b, 0 <= s < queries,
+ * is at position p = T_b - queries + s and sees the tokens i with
+ *   i <= p  and  (i > p - window  or  i < sinks).
+ *   out[b][r][c] = sum_i softmax_i(scale * q[b][r]·k_hat[i]) * v_hat[i][c] over those i.
+ *   q:   device fp16 [batch][q_heads][128]; q_heads = kv_heads * queries * G; row
+ *        (h*queries + s)*G + g is query head g of kv head h at position s.
+ *        queries * G in {1,2,4,8,16,32,64}.
+ *   out: device fp32 [batch][q_heads][128].  A row that sees no token is zero.
+ * window >= 1 (window >= T_b: all tokens up to p), sinks >= 0.  Blocks that no query
+ * sees are not read: they may have been freed.  The tokens inside a block are reordered,
+ * so a block that is seen in part is masked through cache->perm, which must be set
+ * unless reorder_key is PACKKV_KEY_IDENTITY (PACKKV_ERR_INVALID_ARG).  A seen block with
+ * an invalid or freed index entry sets PACKKV_DEV_BAD_RECORD and its tokens are left
+ * out.  ws as for packkv_attention_decode (packkv_attention_window_workspace_bytes); results
+ * do not depend on the launch's timing.
+ */
+size_t packkv_attention_window_workspace_bytes(const packkv_cache* cache, int32_t q_heads);
+packkv_status packkv_attention_window(const packkv_cache* cache, const uint16_t* q, int32_t q_heads,
+                                      int32_t queries, int32_t window, int32_t sinks, float scale, float* out,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ---- The cache's blocks --------------------------------------------------------------
+ * Records are never rewritten, so two index entries may name one record: a sequence is
+ * forked by copying entries, blocks are given up by marking entries, and the room of
+ * records that no entry names is taken back by copying the live ones.  Batches of more
+ * than PACKKV_RAGGED_MAX_BATCH sequences are PACKKV_ERR_UNSUPPORTED in all three calls.
+ */
+
+/*
+ * Sequence dst[i] becomes a copy of sequence src[i], i < n (host arrays): its first
+ * blocks' index entries (at the physical blocks the block table gives dst[i], which no
+ * other sequence may share), permutations, tail tokens and counters.  No record moves.
+ * Every dst at most once and none of them a src, all in range (PACKKV_ERR_INVALID_ARG).
+ * One src may have several dst.  What dst held is forgotten.
+ */
+packkv_status packkv_fork_sequences(packkv_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
+                                    void* stream);
+
+/*
+ * Gives up the logical blocks first[b] .. first[b] + count[b] - 1 of every sequence b
+ * (host int32 [batch]; count 0: none) for all heads: their index entries become
+ * {0xFFFFFFFF, 0}.  Counters and positions stay, so a window that has moved on reads
+ * as before; a call that reads a freed block treats it as an invalid entry
+ * (PACKKV_DEV_BAD_RECORD).  A physical block that another sequence shares through the
+ * block table is given up for it too.  0 <= first, first + count <= the sequence's
+ * blocks (PACKKV_ERR_INVALID_ARG, nothing launched).  A sequence that is done: free its
+ * blocks, then set its counters to 0.
+ */
+packkv_status packkv_free_blocks(packkv_cache* cache, const int32_t* first, const int32_t* count, void* stream);
+
+/*
+ * Copies what src's sequences hold into dst, records packed from the start of dst's
+ * arenas in (sequence, head, block) order of their first entry, a record that several
+ * entries name once.  dst: a cache of the same format, batch and kv_heads whose buffers
+ * src does not use, with max_blocks >= src's blocks; both ragged or both uniform; a
+ * block table may belong to either (dst's gives blocks that src holds apart distinct
+ * physical blocks).  Freed entries stay freed; dst->perm (if set, src->perm must be)
+ * and the tails up to each length are copied; dst's arena ends and counters are set.
+ * The rest of dst is left as it was.  If the records do not fit dst's arenas,
+ * PACKKV_DEV_CAPACITY is set in dst, its ends are 0 and every copied entry is invalid;
+ * an invalid entry of src sets PACKKV_DEV_BAD_RECORD in dst and is copied as freed.
+ *   ws: device, 16-byte aligned, ws_bytes >= packkv_compact_workspace_bytes(src); no
+ *       initialisation needed; calls that share it must not overlap in time.
+ */
+size_t packkv_compact_workspace_bytes(const packkv_cache* src);
+packkv_status packkv_compact(packkv_cache* dst, const packkv_cache* src, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, returns PACKKV_OK if no device status bit is set,
  * else PACKKV_ERR_CAPACITY (capacity bit set) or PACKKV_ERR_DEVICE; stores
  * the bits in *bits_out (if not NULL) and clears them. */

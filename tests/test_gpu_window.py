@@ -1,0 +1,213 @@
+"""packkv_attention_window against the oracle: sliding windows with first tokens that stay
+visible, one and several query positions, ragged batches, block tables, freed blocks.
+
+Tolerance: the repository's own, 1e-3 * sum|terms| per element, and on the whole output a
+relative 2-norm of 1e-5: the scores' integer products carry q' to 2^-22 of its largest
+value or better (three digits), which leaves scores of these inputs (|q'| up to about 16,
+128 channels, codes up to 15 with a spread of about 3, scale 0.09) off by
+0.09 * sqrt(128) * 3 * 16 * 2^-22 / sqrt(3) = 7e-6 on average, and an output by about as much.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from decode_gemv_packkv_b200 import synth
+from parity_util import assert_within_terms, to_dev
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 1.0 / np.sqrt(128.0)
+
+
+@pytest.fixture(scope="module")
+def pk():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_gemv_packkv_b200 import packkv
+    return packkv
+
+
+def _caches(pk, B, H, bits, tokens, seed, structured=False, key=O.KEY_K_SUM, mb=None):
+    """A ragged GPU cache and its oracle with tokens[b] tokens in sequence b."""
+    T = max(max(tokens), 1)
+    k, v, _ = synth.small_case(seed, B, H, 1, T, structured=structured)
+    nb = [t // 128 for t in tokens]
+    mb = mb or max(max(nb), 1)
+    cache = pk.PackKVCache(B, H, mb, bits, reorder_key=key, ragged=True, keep_perm=True)
+    oc = O.RaggedOracleCache(B, H, mb, bits, key)
+    most = max(nb)
+    if most:
+        pk.packkv_encode_block(cache, to_dev(k[:, :, :most * 128]), to_dev(v[:, :, :most * 128]), most)
+        oc.encode_blocks_ragged(k[:, :, :most * 128], v[:, :, :most * 128], most)
+    cache.set_lengths(nb, [0] * B)
+    oc.seq_blocks, oc.seq_tail = list(nb), [t % 128 for t in tokens]
+    for b, t in enumerate(tokens):
+        oc.k_tail[b, :, :t % 128] = k[b, :, nb[b] * 128:t]
+        oc.v_tail[b, :, :t % 128] = v[b, :, nb[b] * 128:t]
+    cache.k_tail.copy_(to_dev(oc.k_tail))
+    cache.v_tail.copy_(to_dev(oc.v_tail))
+    cache.set_lengths(nb, oc.seq_tail)
+    return cache, oc
+
+
+def _queries(B, rows, seed):
+    return np.random.default_rng(seed).standard_normal((B, rows, 128)).astype(np.float16)
+
+
+def _check(pk, cache, oc, rows, queries, window, sinks, seed, what=""):
+    q = _queries(oc.batch, oc.kv_heads * rows, seed)
+    out = torch.full(q.shape, 7.0, device="cuda")
+    pk.packkv_attention_window(cache, to_dev(q), SCALE, out, window, sinks=sinks, queries=queries)
+    ref, terms = O.window_attention(oc, q, SCALE, window, sinks, queries)
+    got = out.double().cpu().numpy()
+    assert_within_terms(got, ref, terms, f"{what} window {window} sinks {sinks}")
+    norm = np.linalg.norm(ref)
+    assert np.linalg.norm(got - ref) <= 1e-5 * norm
+    assert pk.packkv_get_status(cache) == 0
+    return out
+
+
+# bits, rows per kv head, queries, structured
+SHAPES = [(4, 1, 1, False), (4, 4, 1, True), (3, 2, 2, False), (2, 8, 4, True), (3, 8, 1, True), (4, 16, 4, False),
+          (2, 1, 1, True), (2, 64, 8, False), (3, 4, 4, True), (4, 2, 1, True)]
+
+
+@pytest.mark.parametrize("bits,rows,queries,structured", SHAPES)
+def test_windows_over_ragged_lengths(pk, bits, rows, queries, structured):
+    """Lengths of nothing, one token, less than the queries, whole blocks, and tails; windows
+    that end inside blocks, hold one token, and hold everything."""
+    cache, oc = _caches(pk, 6, 2, bits, [700, 0, 1, 3, 256, 399], 40 + bits + rows, structured)
+    for window, sinks in [(300, 4), (1, 0), (128, 0), (100000, 0), (129, 130), (37, 1)]:
+        _check(pk, cache, oc, rows, queries, window, sinks, window, f"{bits} bits, {rows} rows")
+
+
+@pytest.mark.parametrize("tokens", [127, 128, 129, 159, 160, 161, 255, 383])
+def test_borders_of_tail_and_window(pk, tokens):
+    cache, oc = _caches(pk, 1, 1, 4, [tokens], tokens)
+    for window in (1, 31, 32, 33, 127, 128, 129, tokens - 1, tokens, tokens + 1):
+        _check(pk, cache, oc, 2, 2, window, 0, window)
+        _check(pk, cache, oc, 1, 1, window, 5, window)
+
+
+def test_large_limits(pk):
+    cache, oc = _caches(pk, 2, 1, 2, [300, 70], 3)
+    big = (1 << 31) - 1
+    for window, sinks in [(big, 0), (1, big), (big, big)]:
+        _check(pk, cache, oc, 1, 1, window, sinks, 1)
+        _check(pk, cache, oc, 8, 8, window, sinks, 2)
+
+
+def test_uniform_batch_and_identity_order(pk):
+    """A uniform batch (no ragged counters), and an unreordered cache without permutations;
+    with everything in the window the result is packkv_attention_decode's to rounding."""
+    B, H, T = 2, 3, 500
+    k, v, _ = synth.small_case(77, B, H, 1, T)
+    cache = pk.PackKVCache(B, H, 4, 4, reorder_key=pk.KEY_IDENTITY)
+    pk.prefill(cache, to_dev(k), to_dev(v))
+    oc = O.RaggedOracleCache(B, H, 4, 4, O.KEY_IDENTITY)
+    oc.encode_blocks_ragged(k[:, :, :384], v[:, :, :384], 3)
+    for t in range(384, T):
+        oc.append_token_ragged(k[:, :, t], v[:, :, t])
+    _check(pk, cache, oc, 4, 2, 200, 3, 1)
+    out = _check(pk, cache, oc, 4, 1, T, 0, 9)
+    full = torch.empty_like(out)
+    pk.packkv_attention_decode(cache, to_dev(_queries(B, H * 4, 9)), SCALE, full)
+    assert torch.linalg.norm(out - full) <= 2e-5 * torch.linalg.norm(full)
+
+
+def test_reordered_cache_needs_its_permutations(pk):
+    cache = pk.PackKVCache(1, 1, 1, 4)
+    q = torch.zeros((1, 1, 128), dtype=torch.float16, device="cuda")
+    with pytest.raises(pk.PackKVError) as e:
+        pk.packkv_attention_window(cache, q, 1.0, torch.empty((1, 1, 128), device="cuda"), 8)
+    assert e.value.status == pk.ERR_INVALID_ARG
+
+
+def test_block_table(pk):
+    """Shared and permuted physical blocks."""
+    cache, oc = _caches(pk, 3, 2, 3, [600, 300, 290], 12, True, mb=5)
+    table = np.arange(15, dtype=np.int32).reshape(3, 5)
+    table[2, :2] = table[0, :2]
+    table[0, :4] = [3, 1, 0, 2]
+    oc.table = table.astype(np.int64)
+    oc._decoded.clear()
+    cache.block_table = torch.from_numpy(table).cuda()
+    cache.s.block_table = cache.block_table.data_ptr()
+    for window, sinks in [(200, 4), (1000, 0), (10, 140)]:
+        _check(pk, cache, oc, 4, 2, window, sinks, window)
+
+
+def test_freed_blocks_behind_the_window(pk):
+    """Blocks that no query sees may be freed; a freed block that one sees is reported and
+    its tokens are left out."""
+    cache, oc = _caches(pk, 2, 2, 4, [1100, 900], 31)
+    pk.packkv_free_blocks(cache, [1, 1], [5, 3])   # sequence 0: blocks 1..5, 1: 1..3
+    out = _check(pk, cache, oc, 2, 1, 300, 4, 5)
+    q = to_dev(_queries(2, 4, 5))
+    pk.packkv_attention_window(cache, q, SCALE, out, 400, sinks=4)   # sequence 0's block 5 is seen
+    assert pk.packkv_get_status(cache) & pk.DEV_BAD_RECORD
+    keep = torch.isfinite(out)
+    assert torch.all(keep)
+
+
+def test_masked_infinities_do_not_spread(pk):
+    """Infinite and NaN tail values behind a query's position leave its output alone."""
+    cache, oc = _caches(pk, 1, 2, 4, [200], 8)
+    q = to_dev(_queries(1, 2 * 4, 3))
+    clean = torch.empty((1, 8, 128), device="cuda")
+    pk.packkv_attention_window(cache, q, SCALE, clean, 64, queries=4)
+    cache.v_tail[0, 0, 71, 5] = float("inf")    # the last token: only the last query sees it
+    cache.v_tail[0, 1, 70, 9] = float("nan")
+    cache.k_tail[0, 1, 71, 7] = float("nan")
+    out = torch.empty_like(clean)
+    pk.packkv_attention_window(cache, q, SCALE, out, 64, queries=4)
+    same = torch.isclose(out, clean, rtol=1e-5, atol=1e-6)
+    assert torch.all(same[0, :3])                # kv head 0, positions 0..2
+    assert torch.isinf(out[0, 3, 5]) and torch.all(torch.isfinite(out[0, 3, 6:]))
+    assert torch.all(same[0, 4:6])               # kv head 1, positions 0..1
+    assert torch.isnan(out[0, 6, 9]) and torch.all(torch.isfinite(out[0, 6, 10:]))
+    assert torch.all(torch.isnan(out[0, 7]))     # a NaN key that it sees
+
+
+def test_nan_and_infinite_queries(pk):
+    cache, _ = _caches(pk, 1, 1, 3, [300], 4)
+    q = torch.randn(1, 2, 128, device="cuda").half()
+    clean = torch.empty((1, 2, 128), device="cuda")
+    pk.packkv_attention_window(cache, q, SCALE, clean, 200)
+    q[0, 1, 3] = float("nan")
+    out = torch.empty_like(clean)
+    pk.packkv_attention_window(cache, q, SCALE, out, 200)
+    assert torch.equal(out[0, 0], clean[0, 0]) and torch.all(torch.isnan(out[0, 1]))
+
+
+def test_repeatable_and_in_a_graph(pk):
+    """The same bits every time, eager and replayed, on a stream of its own."""
+    cache, oc = _caches(pk, 3, 4, 4, [3000, 1300, 90], 6)
+    q = to_dev(_queries(3, 16, 1))
+    out = torch.empty((3, 16, 128), device="cuda")
+    pk.packkv_attention_window(cache, q, SCALE, out, 1500, sinks=4)
+    want = out.clone()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        out.zero_()
+        stream.wait_stream(torch.cuda.current_stream())
+        pk.packkv_attention_window(cache, q, SCALE, out, 1500, sinks=4, stream=stream)
+        torch.cuda.current_stream().wait_stream(stream)
+        assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pk.packkv_attention_window(cache, q, SCALE, out, 1500, sinks=4)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_many_rows(pk):
+    """More rows than the device holds at once, and a long row on its own."""
+    cache, oc = _caches(pk, 20, 16, 2, [260 + 3 * b for b in range(20)], 15)
+    _check(pk, cache, oc, 1, 1, 200, 4, 1)
+    cache, oc = _caches(pk, 1, 1, 3, [128 * 70 + 77], 16)
+    _check(pk, cache, oc, 2, 1, 8500, 4, 2)
