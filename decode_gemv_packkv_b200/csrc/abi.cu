@@ -25,6 +25,7 @@ using packkv::RaggedEncodePlan;
 using packkv::RaggedPlan;
 using packkv::RangePlan;
 using packkv::WindowArgs;
+using packkv::WindowPlan;
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -655,15 +656,11 @@ packkv_status packkv_attention_window(const packkv_cache* cache, const uint16_t*
   a.scale = scale;
   a.out = out;
   a.partials = reinterpret_cast<float*>(ws);
-  if (!is_ragged(cache)) {
-    a.most_items = packkv::window_items(a, a.n_blocks, a.tail_len);
-    return cuda_status(packkv::launch_window(a, nullptr, as_stream(stream)));
-  }
-  LengthPlan& plan = plan_of<LengthPlan>();
-  fill_lengths(cache, plan);
+  if (!is_ragged(cache)) return cuda_status(packkv::launch_window(a, nullptr, as_stream(stream)));
+  WindowPlan& plan = plan_of<WindowPlan>();
   for (int b = 0; b < cache->batch; ++b) {
-    const int n = packkv::window_items(a, plan.blocks[b], plan.tail[b]);
-    a.most_items = n > a.most_items ? n : a.most_items;
+    plan.blocks[b] = cache->seq_blocks[b];
+    plan.tail[b] = (uint8_t)cache->seq_tail[b];
   }
   return cuda_status(packkv::launch_window(a, &plan, as_stream(stream)));
 }

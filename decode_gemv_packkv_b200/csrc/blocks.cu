@@ -41,34 +41,53 @@ __device__ __forceinline__ unsigned long long* entry_ptr(uint32_t* index, long e
   return reinterpret_cast<unsigned long long*>(index) + e;
 }
 
-// Copies n uint4 with the whole CTA.
+// Copies n uint4 with the whole CTA, four loads in flight per thread.
 __device__ __forceinline__ void copy16(void* dst, const void* src, int n) {
   uint4* d = reinterpret_cast<uint4*>(dst);
   const uint4* s = reinterpret_cast<const uint4*>(src);
-  for (int i = threadIdx.x; i < n; i += blockDim.x) d[i] = s[i];
+  for (int i0 = threadIdx.x; i0 < n; i0 += 4 * blockDim.x) {
+    uint4 r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k * (int)blockDim.x < n) r[k] = s[i0 + k * blockDim.x];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k * (int)blockDim.x < n) d[i0 + k * blockDim.x] = r[k];
+  }
 }
 
-// One CTA per (pair, head): entries, permutations and tail of src's blocks.
+// Three CTAs per (pair, head): the K tail, the V tail, and the blocks' entries and
+// permutations.
 __global__ void __launch_bounds__(256) fork_kernel(const packkv_cache c, const __grid_constant__ PairPlan plan) {
-  const int i = blockIdx.x / c.kv_heads, h = blockIdx.x % c.kv_heads;
-  const int src = plan.src[i], dst = plan.dst[i], nb = plan.blocks[i], tail = plan.tail[i];
+  const int part = blockIdx.x % 3, ih = blockIdx.x / 3;
+  const int i = ih / c.kv_heads, h = ih % c.kv_heads;
+  const int src = plan.src[i], dst = plan.dst[i];
+  if (part < 2) {
+    const size_t ts = ((size_t)src * c.kv_heads + h) * 128 * 128, td = ((size_t)dst * c.kv_heads + h) * 128 * 128;
+    uint16_t* tail = part == 0 ? c.k_tail : c.v_tail;
+    copy16(tail + td, tail + ts, plan.tail[i] * 16);
+    return;
+  }
+  const int nb = plan.blocks[i];
   for (int j = threadIdx.x; j < nb; j += blockDim.x) {
     const long from = entry_at(c, src, h, j), to = entry_at(c, dst, h, j);
     if (to < 0) continue;
-    *entry_ptr(c.k_index, to) = from < 0 ? kFreedEntry : *entry_ptr(c.k_index, from);
-    *entry_ptr(c.v_index, to) = from < 0 ? kFreedEntry : *entry_ptr(c.v_index, from);
+    const unsigned long long ke = from < 0 ? kFreedEntry : *entry_ptr(c.k_index, from);
+    const unsigned long long ve = from < 0 ? kFreedEntry : *entry_ptr(c.v_index, from);
+    *entry_ptr(c.k_index, to) = ke;
+    *entry_ptr(c.v_index, to) = ve;
   }
-  if (c.perm != nullptr) {
-    for (int x = threadIdx.x; x < nb * 8; x += blockDim.x) {  // 128 bytes of a block: 8 uint4
-      const int j = x >> 3, k = x & 7;
-      const long from = entry_at(c, src, h, j), to = entry_at(c, dst, h, j);
-      if (from < 0 || to < 0) continue;
-      reinterpret_cast<uint4*>(c.perm + to * 128)[k] = reinterpret_cast<const uint4*>(c.perm + from * 128)[k];
-    }
+  if (c.perm == nullptr) return;
+  if (c.block_table == nullptr) {  // the rows' permutations lie side by side
+    copy16(c.perm + entry_at(c, dst, h, 0) * 128, c.perm + entry_at(c, src, h, 0) * 128, nb * 8);
+    return;
   }
-  const size_t ts = ((size_t)src * c.kv_heads + h) * 128 * 128, td = ((size_t)dst * c.kv_heads + h) * 128 * 128;
-  copy16(c.k_tail + td, c.k_tail + ts, tail * 16);
-  copy16(c.v_tail + td, c.v_tail + ts, tail * 16);
+  for (int x = threadIdx.x; x < nb * 8; x += blockDim.x) {  // 128 bytes of a block: 8 uint4
+    const int j = x >> 3, k = x & 7;
+    const long from = entry_at(c, src, h, j), to = entry_at(c, dst, h, j);
+    if (from < 0 || to < 0) continue;
+    reinterpret_cast<uint4*>(c.perm + to * 128)[k] = reinterpret_cast<const uint4*>(c.perm + from * 128)[k];
+  }
 }
 
 __global__ void __launch_bounds__(128) free_kernel(const packkv_cache c, const __grid_constant__ RangePlan plan) {
@@ -152,6 +171,7 @@ __device__ __forceinline__ bool source_entry(const CompactArgs& a, const LengthP
 }
 
 __global__ void __launch_bounds__(256) mark_kernel(const CompactArgs a, const __grid_constant__ LengthPlan plan) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (x >= 2 * a.entries) return;
   const int tensor = x >= a.entries;
@@ -184,6 +204,8 @@ __global__ void __launch_bounds__(kTile) offsets_kernel(const CompactArgs a, con
   __shared__ uint32_t warp_sums[kTile / 32];
   __shared__ uint32_t my_tile;
   __shared__ unsigned long long before;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tensor = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   if (tid == 0) my_tile = atomicAdd(a.ws.ticket + tensor, 1u);  // every earlier tile's CTA has started
   __syncthreads();
@@ -217,41 +239,103 @@ __global__ void __launch_bounds__(kTile) offsets_kernel(const CompactArgs a, con
   }
   __syncthreads();
   const uint32_t tile_sum = warp_sums[kTile / 32 - 1];
-  if (tid == 0) {
+  if (tid < 32) {  // warp 0 looks back over 32 tiles at a time
     unsigned long long* words = a.ws.tile[tensor];
+    if (tid == 0 && tile > 0) atomicExch(words + tile, kAggregate | tile_sum);
     unsigned long long sum = 0ull;
-    if (tile > 0) {
-      atomicExch(words + tile, kAggregate | tile_sum);
-      const uint64_t start = global_ns();
-      for (int64_t t = (int64_t)tile - 1; t >= 0;) {
-        const unsigned long long w = atomicAdd(words + t, 0ull);
-        if (w == 0ull) {  // not published yet: bounded wait (an earlier CTA that is running)
-          if (global_ns() - start > 1000000000ull) {
-            set_status(a.dst.ctrl, PACKKV_DEV_TIMEOUT);
-            break;
-          }
-          continue;
+    const uint64_t start = global_ns();
+    for (int64_t t = (int64_t)tile - 1; t >= 0;) {
+      const int64_t mine = t - lane;  // lane 0 the nearest
+      const unsigned long long w = mine >= 0 ? atomicAdd(words + mine, 0ull) : kPrefix;
+      if (__any_sync(0xffffffffu, w == 0ull)) {  // not published yet: bounded wait (a CTA that is running)
+        if (__any_sync(0xffffffffu, global_ns() - start > 1000000000ull)) {
+          if (lane == 0) set_status(a.dst.ctrl, PACKKV_DEV_TIMEOUT);
+          break;
         }
-        sum += w & kValue;
-        if (w & kPrefix) break;
-        --t;
+        continue;
       }
+      const uint32_t done = __ballot_sync(0xffffffffu, (w & kPrefix) != 0ull);
+      unsigned long long add = done == 0u || lane <= __ffs(done) - 1 ? w & kValue : 0ull;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+      sum += add;
+      if (done) break;
+      t -= 32;
     }
-    atomicExch(words + tile, kPrefix | (sum + tile_sum));
-    before = sum;
-    if ((int64_t)(tile + 1) * kTile >= a.entries) a.ws.total[tensor] = sum + tile_sum;
+    if (tid == 0) {
+      atomicExch(words + tile, kPrefix | (sum + tile_sum));
+      before = sum;
+      if ((int64_t)(tile + 1) * kTile >= a.entries) a.ws.total[tensor] = sum + tile_sum;
+    }
   }
   __syncthreads();
   if (len != 0u)
     a.ws.moved[tensor][e] = (uint32_t)(before + incl - len + (tid >= 32 ? warp_sums[(tid >> 5) - 1] : 0u));
 }
 
-// Copies: a warp per entry of either tensor (its record if it owns one, the new entry),
-// then a warp per (row, 32 tail tokens) and the permutations.
-__global__ void __launch_bounds__(256) move_kernel(const CompactArgs a, const __grid_constant__ LengthPlan plan) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
-  const int64_t warp0 = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+// ---- the copy ----
+// A warp takes batches of four entries of both tensors: eight lanes look their entries
+// up side by side and write the new ones, then lane 0 moves the owned records through
+// three shared-memory stages with bulk copies (a load and a store in flight at a time).
+constexpr int kMoveWarps = 4;
+constexpr int kMoveStages = 3;
+constexpr int kBatch = 4;
+
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+struct Mover {  // lane 0's pipeline: load n goes to stage n % 3, store n - 1 is issued after it
+  unsigned char* stage;
+  uint32_t stage_bytes;
+  uint64_t* bar;
+  uint64_t* ctrl;
+  long n;         // loads issued
+  void* dst;      // of load n - 1, whose store is not issued yet
+  uint32_t bytes;
+  bool dead;      // a load gave up: nothing more is moved
+
+  __device__ void store_last() {
+    if (n == 0 || dead) return;
+    const int s = (int)((n - 1) % kMoveStages);
+    if (!mbar_wait_bounded(bar + s, (uint32_t)(((n - 1) / kMoveStages) & 1), ctrl)) {
+      dead = true;
+      return;
+    }
+    bulk_s2g(dst, stage + s * stage_bytes, bytes);
+  }
+  __device__ void move(void* to, const void* from, uint32_t nbytes) {
+    if (dead) return;
+    const int s = (int)(n % kMoveStages);
+    // stores up to n - 2 are issued; the stage held record n - 3
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    mbar_arrive_expect_tx(bar + s, nbytes);
+    bulk_g2s(stage + s * stage_bytes, from, nbytes, bar + s);
+    store_last();
+    ++n;
+    dst = to;
+    bytes = nbytes;
+  }
+  __device__ void finish() {
+    store_last();
+    if (dead && n > 0) {  // wait, bounded, for the other load in flight
+      const int s = (int)(n % kMoveStages);
+      mbar_wait_bounded(bar + s, (uint32_t)((n / kMoveStages) & 1), ctrl);
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+};
+
+__global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const CompactArgs a, uint32_t stage_bytes,
+                                                              const __grid_constant__ LengthPlan plan) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t bars[kMoveWarps][kMoveStages];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t warps = (int64_t)gridDim.x * kMoveWarps;
+  const int64_t warp0 = (int64_t)warp * gridDim.x + blockIdx.x;  // neighbours in the list go to different SMs
   const unsigned long long total_k = a.ws.total[0], total_v = a.ws.total[1];
   const unsigned long long room = a.dst.arena_bytes / 16;
   const bool fits = total_k <= room && total_v <= room;
@@ -261,55 +345,82 @@ __global__ void __launch_bounds__(256) move_kernel(const CompactArgs a, const __
     a.dst.ctrl[kCtrlScratch] = 0ull;
     if (!fits) set_status(a.dst.ctrl, PACKKV_DEV_CAPACITY);
   }
-  for (int64_t x = warp0; x < 2 * a.entries; x += warps) {
-    const int tensor = (int)(x & 1);
-    const int64_t e = x >> 1;
-    uint2 r;
-    long at = -1;
-    bool bad;
-    if (!source_entry(a, plan, tensor, e, &r, &at, &bad)) continue;
-    const int row = (int)(e / a.most), j = (int)(e - (int64_t)row * a.most);
-    const int b = row / a.src.kv_heads, h = row - b * a.src.kv_heads;
-    const long to = entry_at(a.dst, b, h, j);
-    unsigned long long entry = kFreedEntry;
-    if (r.x != kFreed && fits) {
-      int64_t first;
-      const bool own = owns_record(a, plan, tensor, e, r, &first);
-      if (first < 0) {
-        bad = true;
-      } else {
-        const uint32_t off = a.ws.moved[tensor][first];
-        if (off + (uint64_t)r.y > room) continue;  // only after a look-back that gave up (status set)
-        entry = (unsigned long long)off | ((unsigned long long)r.y << 32);
-        if (own) {
-          const uint4* s = reinterpret_cast<const uint4*>(tensor ? a.src.v_arena : a.src.k_arena) + r.x;
-          uint4* d = reinterpret_cast<uint4*>(tensor ? a.dst.v_arena : a.dst.k_arena) + off;
-#pragma unroll 4
-          for (uint32_t i = lane; i < r.y; i += 32) __stcs(d + i, __ldcs(s + i));
+  if (lane == 0) {
+    for (int s = 0; s < kMoveStages; ++s) mbar_init(&bars[warp][s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  Mover mv{smem + warp * kMoveStages * stage_bytes, stage_bytes, bars[warp], a.dst.ctrl, 0, nullptr, 0u, false};
+  const int64_t batches = (a.entries + kBatch - 1) / kBatch;
+  for (int64_t x = warp0; x < batches; x += warps) {
+    const int tensor = (lane / kBatch) & 1;
+    const int64_t e = x * kBatch + lane % kBatch;
+    uint2 r = make_uint2(kFreed, 0u);
+    long at = -1, to = -1;
+    bool bad = false, own = false, live = false;
+    uint32_t off = 0u;
+    if (lane < 2 * kBatch && e < a.entries) live = source_entry(a, plan, tensor, e, &r, &at, &bad);
+    if (live) {
+      const int row = (int)(e / a.most), j = (int)(e - (int64_t)row * a.most);
+      const int b = row / a.src.kv_heads;
+      to = entry_at(a.dst, b, row - b * a.src.kv_heads, j);
+      unsigned long long entry = kFreedEntry;
+      if (r.x != kFreed && fits) {
+        int64_t first;
+        own = owns_record(a, plan, tensor, e, r, &first);
+        if (first < 0) {
+          bad = true;
+        } else {
+          off = a.ws.moved[tensor][first];
+          entry = (unsigned long long)off | ((unsigned long long)r.y << 32);
+          own = own && off + (uint64_t)r.y <= room;  // always, unless the look-back gave up (status set)
         }
       }
+      if (bad) set_status(a.dst.ctrl, PACKKV_DEV_BAD_RECORD);
+      if (to >= 0) *entry_ptr(tensor ? a.dst.v_index : a.dst.k_index, to) = entry;
     }
-    if (bad && lane == 0) set_status(a.dst.ctrl, PACKKV_DEV_BAD_RECORD);
-    if (to < 0) continue;
-    if (lane == 0) *entry_ptr(tensor ? a.dst.v_index : a.dst.k_index, to) = entry;
-    if (tensor == 0 && a.dst.perm != nullptr && at >= 0 && lane < 8)
-      reinterpret_cast<uint4*>(a.dst.perm + to * 128)[lane] =
-          reinterpret_cast<const uint4*>(a.src.perm + at * 128)[lane];
+    uint32_t todo = __ballot_sync(0xffffffffu, own);
+    while (todo) {
+      const int k = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const uint32_t so = __shfl_sync(0xffffffffu, r.x, k), n16 = __shfl_sync(0xffffffffu, r.y, k);
+      const uint32_t dof = __shfl_sync(0xffffffffu, off, k);
+      if (lane == 0)
+        mv.move((k >= kBatch ? a.dst.v_arena : a.dst.k_arena) + (uint64_t)dof * 16,
+                (k >= kBatch ? a.src.v_arena : a.src.k_arena) + (uint64_t)so * 16, n16 * 16u);
+    }
+    if (a.dst.perm != nullptr) {
+      const int k = lane >> 3;  // four entries, eight lanes each
+      const long from = __shfl_sync(0xffffffffu, at, k), dest = __shfl_sync(0xffffffffu, to, k);
+      if (from >= 0 && dest >= 0)
+        reinterpret_cast<uint4*>(a.dst.perm + dest * 128)[lane & 7] =
+            reinterpret_cast<const uint4*>(a.src.perm + from * 128)[lane & 7];
+    }
   }
-  // tails: 32 tokens (512 uint4) per task
+  // tails: 32 tokens (512 uint4) of K or V per task
   const int64_t rows = (int64_t)a.src.batch * a.src.kv_heads;
   for (int64_t x = warp0; x < rows * 8; x += warps) {
     const int64_t row = x >> 3;
     const int part = (int)(x & 3);
-    const int tail = plan.tail[row / a.src.kv_heads];
-    const uint16_t* s = (x & 4) ? a.src.v_tail : a.src.k_tail;
-    uint16_t* d = (x & 4) ? a.dst.v_tail : a.dst.k_tail;
-    const uint4* s4 = reinterpret_cast<const uint4*>(s + row * 128 * 128) + part * 512;
-    uint4* d4 = reinterpret_cast<uint4*>(d + row * 128 * 128) + part * 512;
-    const int n = min(512, tail * 16 - part * 512);
-#pragma unroll 4
-    for (int i = lane; i < n; i += 32) d4[i] = s4[i];
+    const int n = min(512, plan.tail[row / a.src.kv_heads] * 16 - part * 512);
+    const uint4* s = reinterpret_cast<const uint4*>(((x & 4) ? a.src.v_tail : a.src.k_tail) + row * 128 * 128) + part * 512;
+    uint4* d = reinterpret_cast<uint4*>(((x & 4) ? a.dst.v_tail : a.dst.k_tail) + row * 128 * 128) + part * 512;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int q = (half * 8 + i) * 32 + lane;
+        if (q < n) v[i] = __ldcs(s + q);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int q = (half * 8 + i) * 32 + lane;
+        if (q < n) __stcs(d + q, v[i]);
+      }
+    }
   }
+  if (lane == 0) mv.finish();
 }
 
 cudaError_t sm_count(int* sms) {
@@ -322,7 +433,7 @@ cudaError_t sm_count(int* sms) {
 }  // namespace
 
 cudaError_t launch_fork(const packkv_cache& c, const PairPlan& plan, int n, cudaStream_t stream) {
-  fork_kernel<<<(unsigned)(n * c.kv_heads), 256, 0, stream>>>(c, plan);
+  fork_kernel<<<(unsigned)(3 * n * c.kv_heads), 256, 0, stream>>>(c, plan);
   return cudaGetLastError();
 }
 
@@ -345,14 +456,32 @@ cudaError_t launch_compact(const packkv_cache& dst, const packkv_cache& src, con
   cudaError_t e = cudaMemsetAsync(ws, 0, a.ws.clear_bytes, stream);
   if (e != cudaSuccess) return e;
   mark_kernel<<<(unsigned)((2 * a.entries + 255) / 256), 256, 0, stream>>>(a, plan);
-  offsets_kernel<<<dim3((unsigned)((a.entries + kTile - 1) / kTile), 2), kTile, 0, stream>>>(a, plan);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the two that follow start while the one before drains (griddepcontrol.wait in each)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((a.entries + kTile - 1) / kTile), 2);
+  cfg.blockDim = dim3(kTile);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, &offsets_kernel, a, plan);
+  if (e != cudaSuccess) return e;
   int sms = 148;
   e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  int64_t grid = (2 * a.entries + 7) / 8;
-  if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
-  move_kernel<<<(unsigned)grid, 256, 0, stream>>>(a, plan);
-  return cudaGetLastError();
+  const uint32_t stage = (uint32_t)raw_record_bytes((int)src.fmt.bits);
+  const size_t smem = (size_t)kMoveWarps * kMoveStages * stage;
+  e = cudaFuncSetAttribute(&move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveWarps * kMoveStages * 8720);
+  if (e != cudaSuccess) return e;
+  const int64_t tasks = (a.entries + kBatch - 1) / kBatch, want = (tasks + kMoveWarps - 1) / kMoveWarps;
+  cfg.gridDim = dim3((unsigned)(want < 2L * sms ? want : 2L * sms));
+  cfg.blockDim = dim3(kMoveWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, &move_kernel, a, stage, plan);
 }
 
 }  // namespace packkv

@@ -127,6 +127,7 @@ struct HeadsArgs {
   HeadsTensor x[3];  // q, k, v
   int dtype;         // PACKKV_DTYPE_*
   int batch, tokens;
+  int tile;          // tokens of a CTA (set by the launch)
   bool norm;
   float eps;
   const int32_t* positions;  // [batch][tokens] or NULL (first + t)
@@ -178,15 +179,22 @@ struct WindowArgs {
   int rows;                 // query rows per kv head: queries * group
   int group, queries, window, sinks;
   int n_blocks, tail_len;   // uniform batches
-  int most_items;           // items of the longest row (seen blocks, pieces of the tail)
+  int most_items;           // items of the longest row (set by launch_window, with the next three)
+  int row_items;            // items of every row (uniform batches)
+  long n_items;             // items of all (row, chunk)s
+  int n_warps;              // warps sharing them
   const uint16_t* q;        // [batch][kv_heads][rows][128]
   float scale;
   float* out;
   float* partials;
 };
+struct WindowPlan {  // ragged batches: what every sequence holds, and its rows' first item
+  int32_t blocks[kMaxRaggedBatch];
+  int32_t base[kMaxRaggedBatch + 1];  // items of the (row, chunk)s of the sequences before
+  uint8_t tail[kMaxRaggedBatch];
+};
 size_t window_workspace_bytes(int batch, int kv_heads, int rows);
-// Items of a row with nb blocks and tl tail tokens (window.cu's item list).
-int window_items(const WindowArgs& a, int nb, int tl);
-cudaError_t launch_window(const WindowArgs& a, const LengthPlan* plan, cudaStream_t stream);
+// plan: blocks and tail of every sequence filled in (ragged batches), or NULL
+cudaError_t launch_window(WindowArgs a, WindowPlan* plan, cudaStream_t stream);
 
 }  // namespace packkv

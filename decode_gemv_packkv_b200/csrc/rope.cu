@@ -25,9 +25,10 @@ namespace packkv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTokTile = 4;                  // tokens of a CTA: one sine and cosine per thread
-constexpr int kRowSlots = kThreads / 16;     // heads in flight per CTA
+constexpr int kThreads = 128;
+constexpr int kRowSlots = kThreads / 16;     // heads side by side in a CTA
+constexpr int kTokTile = kRowSlots;          // most tokens of a CTA: one per half-warp
+constexpr int kDepth = 4;                    // rows a half-warp has in flight
 
 template <class T>
 struct Vec4;  // four consecutive elements
@@ -111,6 +112,7 @@ struct HeadRow {
 template <class T, bool kWide>
 struct RowLoad {  // the loads of a row, before the conversion
   typename Vec4<T>::Raw ra, rb;
+  __device__ void clear() { ra = rb = typename Vec4<T>::Raw{}; }
   __device__ void issue(const T* p, const LaneMap& m) {
     ra = __ldcs(reinterpret_cast<const typename Vec4<T>::Raw*>(p + m.ca[0]));
     rb = __ldcs(reinterpret_cast<const typename Vec4<T>::Raw*>(p + m.cb[0]));
@@ -123,6 +125,10 @@ struct RowLoad {  // the loads of a row, before the conversion
 template <class T>
 struct RowLoad<T, false> {
   T ra[4], rb[4];
+  __device__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ra[i] = rb[i] = T(0.f);
+  }
   __device__ void issue(const T* p, const LaneMap& m) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -155,51 +161,103 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const HeadRow& r, const
   }
 }
 
-// Norm (w = this lane's weights) and rotation of one row; cs = the row's token's table.
-template <bool kHalf>
-__device__ __forceinline__ void turn_row(HeadRow& r, bool norm, float eps, const HeadRow& w, const float2* cs,
-                                         const LaneMap& m, int rot) {
-  if (norm) {
-    float ss = 0.f;
+// What one token does to this lane's channels, the norm's weights folded in: element i of
+// A and B (half layout, a pair) or neighbours (interleaved).
+//   half:        a' = a ca + b sa,  b' = b cb + a sb   with (wa cos, -wb sin, wb cos, wa sin)
+//   interleaved: x' = x c + y s for both members: A in (ca, sa), B in (cb, sb)
+// Pairs that are not turned hold (w, 0), and their rows must not read the s terms (an
+// infinity would spoil its neighbour).
+struct Turn {
+  float2 ca[2], sa[2], cb[2], sb[2];
+  uint32_t on;  // half: bit 0 (all four pairs); interleaved: bits 0, 1 (A), 2, 3 (B)
+};
+
+template <bool kHalf, bool kWide>
+__device__ __forceinline__ Turn lane_turn(const float2* cs, const HeadRow& w, const LaneMap& m, int rot) {
+  Turn u;
+  u.on = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ss = fmaf(r.a[i], r.a[i], fmaf(r.b[i], r.b[i], ss));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);  // within the half-warp
-    const float f = rsqrtf(fmaf(ss, 1.f / 128.f, eps));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.a[i] *= f * w.a[i];
-      r.b[i] *= f * w.b[i];
-    }
-  }
-  // pairs from rot/2 on are left untouched (not multiplied by 1 and 0: an infinity
-  // would spoil its neighbour)
-  if constexpr (kHalf) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    float ca = w.a[i], sa = 0.f, cb = w.b[i], sb = 0.f;
+    if constexpr (kHalf) {
       if (2 * m.pa[i] < rot) {
         const float2 z = cs[m.pa[i]];
-        const float a = r.a[i], b = r.b[i];
-        r.a[i] = a * z.x - b * z.y;
-        r.b[i] = b * z.x + a * z.y;
+        ca = w.a[i] * z.x;
+        sa = -w.b[i] * z.y;
+        cb = w.b[i] * z.x;
+        sb = w.a[i] * z.y;
+        u.on |= 1u << i;
       }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
+    } else {
+      const float sign = (i & 1) ? 1.f : -1.f;  // x' = x cos - y sin, y' = y cos + x sin
       if (2 * m.pa[i] < rot) {
         const float2 z = cs[m.pa[i]];
-        const float a = r.a[i], b = r.a[i + 1];
-        r.a[i] = a * z.x - b * z.y;
-        r.a[i + 1] = b * z.x + a * z.y;
+        ca = w.a[i] * z.x;
+        sa = sign * w.a[i ^ 1] * z.y;
+        u.on |= 1u << (i >> 1);
       }
       if (2 * m.pb[i] < rot) {
         const float2 z = cs[m.pb[i]];
-        const float a = r.b[i], b = r.b[i + 1];
-        r.b[i] = a * z.x - b * z.y;
-        r.b[i + 1] = b * z.x + a * z.y;
+        cb = w.b[i] * z.x;
+        sb = sign * w.b[i ^ 1] * z.y;
+        u.on |= 4u << (i >> 1);
       }
     }
+    float2 *pca = &u.ca[i >> 1], *psa = &u.sa[i >> 1], *pcb = &u.cb[i >> 1], *psb = &u.sb[i >> 1];
+    if (i & 1) {
+      pca->y = ca, psa->y = sa, pcb->y = cb, psb->y = sb;
+    } else {
+      pca->x = ca, psa->x = sa, pcb->x = cb, psb->x = sb;
+    }
+  }
+  return u;
+}
+
+// Norm and rotation of one row.
+template <bool kHalf, bool kWide>
+__device__ __forceinline__ void turn_row(HeadRow& r, bool norm, float eps, const Turn& u) {
+  float2 a[2] = {{r.a[0], r.a[1]}, {r.a[2], r.a[3]}}, b[2] = {{r.b[0], r.b[1]}, {r.b[2], r.b[3]}};
+  if (norm) {
+    float2 s2 = __fmul2_rn(a[0], a[0]);
+    s2 = __ffma2_rn(a[1], a[1], s2);
+    s2 = __ffma2_rn(b[0], b[0], s2);
+    s2 = __ffma2_rn(b[1], b[1], s2);
+    float ss = s2.x + s2.y;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);  // within the half-warp
+    const float f = rsqrtf(fmaf(ss, 1.f / 128.f, eps));
+    const float2 f2 = make_float2(f, f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i] = __fmul2_rn(a[i], f2);
+      b[i] = __fmul2_rn(b[i], f2);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float2 x = __fmul2_rn(a[i], u.ca[i]), y = __fmul2_rn(b[i], u.cb[i]);
+    if constexpr (kHalf && kWide) {
+      if (u.on) {  // the lane's pairs turn all or none
+        x = __ffma2_rn(b[i], u.sa[i], x);
+        y = __ffma2_rn(a[i], u.sb[i], y);
+      }
+    } else if constexpr (kHalf) {
+      if (u.on & (1u << (2 * i))) {
+        x.x = fmaf(b[i].x, u.sa[i].x, x.x);
+        y.x = fmaf(a[i].x, u.sb[i].x, y.x);
+      }
+      if (u.on & (2u << (2 * i))) {
+        x.y = fmaf(b[i].y, u.sa[i].y, x.y);
+        y.y = fmaf(a[i].y, u.sb[i].y, y.y);
+      }
+    } else {
+      if (u.on & (1u << i)) x = __ffma2_rn(make_float2(a[i].y, a[i].x), u.sa[i], x);
+      if (u.on & (4u << i)) y = __ffma2_rn(make_float2(b[i].y, b[i].x), u.sb[i], y);
+    }
+    r.a[2 * i] = x.x;
+    r.a[2 * i + 1] = x.y;
+    r.b[2 * i] = y.x;
+    r.b[2 * i + 1] = y.y;
   }
 }
 
@@ -221,12 +279,12 @@ __device__ __forceinline__ uint32_t length_of(const UniformLength& p, int) { ret
 __device__ __forceinline__ uint32_t length_of(const RaggedLengths& p, int b) { return p.tokens[b]; }
 
 template <class T, bool kHalf, bool kWide, class Plan>
-__global__ void __launch_bounds__(kThreads) heads_kernel(const HeadsArgs a, const __grid_constant__ Plan plan) {
+__global__ void __launch_bounds__(kThreads, !kWide ? 1 : (sizeof(T) == 2 ? 8 : 4)) heads_kernel(const HeadsArgs a, const __grid_constant__ Plan plan) {
   __shared__ float2 table[kTokTile][64];
-  const int tiles = is_append<Plan> ? 1 : (a.tokens + kTokTile - 1) / kTokTile;
+  const int tiles = is_append<Plan> ? 1 : (a.tokens + a.tile - 1) / a.tile;
   const int b = blockIdx.x / tiles;
-  const int t0 = (blockIdx.x - b * tiles) * kTokTile;
-  const int nt = is_append<Plan> ? 1 : min(kTokTile, a.tokens - t0);
+  const int t0 = (blockIdx.x - b * tiles) * a.tile;
+  const int nt = is_append<Plan> ? 1 : min(a.tile, a.tokens - t0);
   const int rot = (int)a.rope.rot_dim;
   uint32_t held = 0;
   if constexpr (is_append<Plan>) {
@@ -251,12 +309,17 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const HeadsArgs a, cons
   const int l = threadIdx.x & 15;
   const LaneMap m = lane_map<kHalf, kWide>(rot, l);
   __syncthreads();
+  // half-warp `slot` takes one token of the tile and every `step`-th head, so its token's
+  // cosines, sines and the weights stay in registers
   const int slot = threadIdx.x >> 4;
+  const int lt = nt > 1 ? 32 - __clz(nt - 1) : 0;  // log2 of the token slots
+  const int ti = slot & ((1 << lt) - 1), h0 = slot >> lt, step = kRowSlots >> lt;
+  const int t = min(ti, nt - 1);
+  const bool mine = ti < nt;
 #pragma unroll 1
   for (int which = 0; which < 3; ++which) {  // q, k, v
     const HeadsTensor& x = a.x[which];
     if (x.data == nullptr) continue;
-    const T* src = reinterpret_cast<const T*>(x.data) + b * x.batch_stride;
     const bool norm = a.norm && which < 2;
     HeadRow w = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}};
     if (norm && x.weight != nullptr) {
@@ -266,22 +329,43 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const HeadsArgs a, cons
         w.b[i] = x.weight[m.cb[i]];
       }
     }
-    const int rows = nt * x.heads;
-    // whole warps stay in the loop (the norm's shuffles); a row past the end repeats the last
-    for (int r0 = 0; r0 < rows; r0 += kRowSlots) {
-      const int r = min(r0 + slot, rows - 1);
-      const int t = r / x.heads, h = r - t * x.heads;
-      RowLoad<T, kWide> in;
-      in.issue(src + (t0 + t) * x.token_stride + h * x.head_stride, m);
-      HeadRow y = in.get();
-      if (which < 2) turn_row<kHalf>(y, norm, a.eps, w, table[t], m, rot);
-      if (r0 + slot < rows) {
-        size_t at;
-        if (!is_append<Plan> || which == 0)
-          at = ((size_t)b * x.heads + h) * a.tokens + t0 + t;
-        else
-          at = ((size_t)b * x.heads + h) * kBlockTokens + (held & (kBlockTokens - 1));
-        store_row<kHalf, kWide>(x.out + at * kHeadDim, y, m);
+    const Turn u = lane_turn<kHalf, kWide>(table[t], w, m, which < 2 ? rot : 0);
+    const T* src = reinterpret_cast<const T*>(x.data) + b * x.batch_stride + (t0 + t) * x.token_stride;
+    uint16_t* dst = x.out;
+    size_t pitch;  // between heads of the output
+    if (!is_append<Plan> || which == 0) {
+      pitch = (size_t)a.tokens * kHeadDim;
+      dst += ((size_t)b * x.heads * a.tokens + t0 + t) * kHeadDim;
+    } else {
+      pitch = (size_t)kBlockTokens * kHeadDim;
+      dst += ((size_t)b * x.heads * kBlockTokens + (held & (kBlockTokens - 1))) * kHeadDim;
+    }
+    // kDepth rows in flight: a row's registers are loaded again as soon as it is converted.
+    // Whole warps stay in the loop (the norm's shuffles); heads past the end are not loaded.
+    src += h0 * x.head_stride;
+    dst += h0 * pitch;
+    const int64_t src_step = step * x.head_stride;
+    const size_t dst_step = step * pitch;
+    int left = x.heads - h0;  // heads from this half-warp's next load on
+    RowLoad<T, kWide> in[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      in[d].clear();
+      if (left > 0) in[d].issue(src, m);
+      left -= step;
+      src += src_step;
+    }
+    for (int hb = 0; hb < x.heads; hb += kDepth * step) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (d > 0 && hb + d * step >= x.heads) break;  // CTA-uniform
+        HeadRow y = in[d].get();
+        if (left > 0) in[d].issue(src, m);
+        if (which < 2) turn_row<kHalf, kWide>(y, norm, a.eps, u);
+        if (mine && left > -kDepth * step) store_row<kHalf, kWide>(dst, y, m);
+        left -= step;
+        src += src_step;
+        dst += dst_step;
       }
     }
   }
@@ -289,7 +373,7 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const HeadsArgs a, cons
 
 template <class T, bool kHalf, bool kWide, class Plan>
 cudaError_t launch_heads_t(const HeadsArgs& a, const Plan& plan, cudaStream_t stream) {
-  const long tiles = is_append<Plan> ? 1 : (a.tokens + (long)kTokTile - 1) / kTokTile;
+  const long tiles = is_append<Plan> ? 1 : (a.tokens + (long)a.tile - 1) / a.tile;
   heads_kernel<T, kHalf, kWide, Plan><<<(unsigned)(tiles * a.batch), kThreads, 0, stream>>>(a, plan);
   return cudaGetLastError();
 }
@@ -325,7 +409,12 @@ cudaError_t launch_heads_p(const HeadsArgs& a, const Plan& plan, cudaStream_t st
 
 }  // namespace
 
-cudaError_t launch_prompt_heads(const HeadsArgs& a, cudaStream_t stream) {
+cudaError_t launch_prompt_heads(const HeadsArgs& args, cudaStream_t stream) {
+  HeadsArgs a = args;
+  // many tokens per CTA amortise a token's sines and weights over all its heads; few
+  // keep every SM busy when there are few tokens
+  const long n = (long)a.batch * a.tokens;
+  a.tile = n >= 8 * 444 ? 8 : (n >= 4 * 148 ? 4 : 1);
   return launch_heads_p(a, PromptPlan{}, stream);
 }
 

@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
+#include <type_traits>
 #include <unordered_map>
 
 #include "decode.cuh"
@@ -85,9 +86,9 @@ __host__ __device__ inline ItemList item_list(int queries, int window, int sinks
 }
 
 __device__ __forceinline__ int row_blocks(const WindowArgs& a, const NoPlan&, int) { return a.n_blocks; }
-__device__ __forceinline__ int row_blocks(const WindowArgs&, const LengthPlan& p, int b) { return p.blocks[b]; }
+__device__ __forceinline__ int row_blocks(const WindowArgs&, const WindowPlan& p, int b) { return p.blocks[b]; }
 __device__ __forceinline__ int row_tail(const WindowArgs& a, const NoPlan&, int) { return a.tail_len; }
-__device__ __forceinline__ int row_tail(const WindowArgs&, const LengthPlan& p, int b) { return p.tail[b]; }
+__device__ __forceinline__ int row_tail(const WindowArgs&, const WindowPlan& p, int b) { return p.tail[b]; }
 
 // What one query row sees, relative to a block's first token.
 __device__ __forceinline__ bool sees(long long pos, long long p, int window, int sinks) {
@@ -543,17 +544,500 @@ __global__ void __launch_bounds__(kWinWarps * 32) window_kernel(const WindowArgs
   if (ranks > 1) cluster.sync();  // no CTA leaves while another reads its sums
 }
 
+// ---- many items: every resident warp takes a contiguous share ----------------------
+// The items of all (row, chunk)s in one list, split evenly over the warps the device
+// holds.  A warp stages an item's K record, then its V record in the same stage (half
+// the shared memory, so more warps per SM), and at each (row, chunk) border writes its
+// sums to the workspace; window_merge_kernel joins them in a fixed order.
+template <int BITS, int G>
+struct FlatCfg {
+  using C = Cfg<BITS, G, false>;
+  static constexpr int kStage = C::kStageRec;
+  static constexpr int kTableBytes = (C::kI8Tab + 15) / 16 * 16;
+  static constexpr int kFixed = kStage + kTableBytes + 1024 * G;
+  static constexpr int kWarpSmem = (kFixed + 32 + 127) / 128 * 128;
+};
+
+template <int BITS, int G>
+struct FlatMem {
+  using F = FlatCfg<BITS, G>;
+  unsigned char* base;
+  __device__ unsigned char* stage() const { return base; }
+  __device__ uint32_t* table() const { return reinterpret_cast<uint32_t*>(base + F::kStage); }
+  __device__ float* scores() const { return reinterpret_cast<float*>(base + F::kStage + F::kTableBytes); }
+  __device__ float* sums() const { return scores() + 128 * G; }
+  __device__ uint64_t* bar(int s) const { return reinterpret_cast<uint64_t*>(base + F::kFixed) + s; }
+};
+
+struct FlatCursor {
+  long bhc;        // (sequence * kv_heads + head) * chunks + chunk
+  int i;           // item of the (row, chunk)
+  ItemList items;  // of the sequence
+};
+
+__device__ __forceinline__ ItemList row_list(const WindowArgs& a, const NoPlan&, int) {
+  return item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len);
+}
+__device__ __forceinline__ ItemList row_list(const WindowArgs& a, const WindowPlan& p, int b) {
+  return item_list(a.queries, a.window, a.sinks, p.blocks[b], p.tail[b]);
+}
+
+// rpc: (row, chunk)s of a sequence.
+__device__ __forceinline__ FlatCursor flat_at(const WindowArgs& a, const NoPlan& p, int, long x) {
+  FlatCursor c;
+  c.items = row_list(a, p, 0);
+  c.bhc = x / c.items.n;
+  c.i = (int)(x - c.bhc * c.items.n);
+  return c;
+}
+__device__ __forceinline__ FlatCursor flat_at(const WindowArgs& a, const WindowPlan& p, int rpc, long x) {
+  int lo = 0, hi = a.batch;  // the last sequence whose first item is <= x has items
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.base[mid] <= x) lo = mid; else hi = mid;
+  }
+  FlatCursor c;
+  c.items = row_list(a, p, lo);
+  const long r = x - p.base[lo];
+  c.bhc = (long)lo * rpc + r / c.items.n;
+  c.i = (int)(r % c.items.n);
+  return c;
+}
+template <class Plan>
+__device__ __forceinline__ void flat_next(const WindowArgs& a, const Plan& p, int rpc, FlatCursor& c) {
+  if (++c.i < c.items.n) return;
+  c.i = 0;
+  ++c.bhc;
+  if constexpr (std::is_same<Plan, WindowPlan>::value) {
+    if (c.bhc % rpc == 0) {  // the next sequence that has items
+      int b = (int)(c.bhc / rpc);
+      while (b < a.batch && p.base[b + 1] == p.base[b]) ++b;
+      if (b < a.batch) c.items = row_list(a, p, b);
+      c.bhc = (long)b * rpc;
+    }
+  }
+}
+
+// Where the index entry and the permutation of a row's logical block j are (-1: the block
+// table names no block).
+__device__ __forceinline__ long entry_of(const WindowArgs& a, int b, int h, int j) {
+  if (a.block_table == nullptr) return ((long)b * a.kv_heads + h) * a.max_blocks + j;
+  const int p = a.block_table[(size_t)b * a.max_blocks + j];
+  if (p < 0 || (long)p >= (long)a.batch * a.max_blocks) return -1;
+  return ((long)(p / a.max_blocks) * a.kv_heads + h) * a.max_blocks + p % a.max_blocks;
+}
+
+// {kind, checked} of an index entry.
+template <int BITS>
+__device__ __forceinline__ int entry_kind(const WindowArgs& a, uint2 e) {
+  constexpr uint32_t raw = (uint32_t)raw_record_bytes(BITS);
+  const bool valid = e.x != 0xFFFFFFFFu && e.y >= 1040 / 16 && e.y * 16u <= raw && (uint64_t)e.x + e.y <= a.arena16;
+  return !valid ? kKindInvalid : (e.y * 16u == raw ? kKindRaw : kKindPacked);
+}
+
+// What a query row sees of the 128 (or fewer) tokens from pos0 on, as bounds on the offset
+// r from pos0: lo < r <= hi, or r < first.
+struct Seen {
+  int lo, hi, first;
+  __device__ bool all() const { return hi >= 127 && (lo < 0 || first > 127); }
+  __device__ bool operator()(int r) const { return r <= hi && (r > lo || r < first); }
+};
+__device__ __forceinline__ int clamp_offset(long long x) { return (int)(x < -1 ? -1 : (x > 128 ? 128 : x)); }
+__device__ __forceinline__ Seen seen_of(long long p, long long pos0, int window, int sinks) {
+  return {clamp_offset(p - window - pos0), clamp_offset(p - pos0), clamp_offset(sinks - pos0)};
+}
+
+// Scores of n <= 32 tail tokens on the CUDA cores: lane = token.
+template <int G>
+__device__ __forceinline__ void flat_tail_scores(const uint16_t* tail, const uint16_t* q, int n, float scale, float* sc,
+                                                 int lane) {
+  float s[G];
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) s[hd] = 0.f;
+  const uint4* row = reinterpret_cast<const uint4*>(tail + (size_t)min(lane, n - 1) * 128);
+#pragma unroll 2
+  for (int c = 0; c < 16; ++c) {
+    const uint4 x = row[c];
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int hd = 0; hd < G; ++hd) {
+      const uint4 y = reinterpret_cast<const uint4*>(q + hd * 128)[c];
+      const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&xw[i]));
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&yw[i]));
+        s[hd] = fmaf(u.x, v.x, s[hd]);
+        s[hd] = fmaf(u.y, v.y, s[hd]);
+      }
+    }
+  }
+  if (lane < n) {
+#pragma unroll
+    for (int hd = 0; hd < G; ++hd) sc[hd * 128 + lane] = scale * s[hd];
+  }
+}
+
+// Adds sum_t p[head][t] v[t][c]: lane = channels 4*lane + i.  Tokens of zero weight (masked
+// ones) are left out, so an infinity or NaN there does not spread.
+template <int G>
+__device__ __forceinline__ void flat_tail_values(const uint16_t* tail, const float* sc, int n, float* sacc, int lane) {
+  float4 s[G];
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) s[hd] = reinterpret_cast<const float4*>(sacc + hd * 128)[lane];
+#pragma unroll 4
+  for (int t = 0; t < n; ++t) {
+    const uint2 x = reinterpret_cast<const uint2*>(tail + (size_t)t * 128)[lane];
+    const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
+#pragma unroll
+    for (int hd = 0; hd < G; ++hd) {
+      const float p = sc[hd * 128 + t];
+      if (p != 0.f) {
+        s[hd].x = fmaf(p, u.x, s[hd].x);
+        s[hd].y = fmaf(p, u.y, s[hd].y);
+        s[hd].z = fmaf(p, v.x, s[hd].z);
+        s[hd].w = fmaf(p, v.y, s[hd].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) reinterpret_cast<float4*>(sacc + hd * 128)[lane] = s[hd];
+  __syncwarp();
+}
+
+constexpr int kPartFloats = 132;  // per (slot, query row): 128 sums, maximum, sum of exp, pad
+
+// Warp sums of the (row, chunk) just done, to slot warp + bhc, and a fresh start.
+template <int G>
+__device__ __forceinline__ void flat_flush(const WindowArgs& a, long bhc, int warp, float* sacc,
+                                           float (&acc_lo)[I8Layout<G>::kNH][8], float (&acc_hi)[I8Layout<G>::kNH][8],
+                                           float (&mp)[G], float (&mrun)[G], float (&lrun)[G], int lane) {
+  using L = I8Layout<G>;
+  const int g = lane >> 2, t = lane & 3;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < L::kNH; ++j) {
+    float* row = sacc + L::head(j, t) * 128 + g;
+#pragma unroll
+    for (int T8 = 0; T8 < 8; ++T8) {
+      if (L::owns(j, t)) {
+        row[16 * T8] += acc_lo[j][T8];
+        row[16 * T8 + 8] += acc_hi[j][T8];
+      }
+      acc_lo[j][T8] = acc_hi[j][T8] = 0.f;
+    }
+  }
+  __syncwarp();
+  float* part = a.partials + (size_t)(warp + bhc) * G * kPartFloats;
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) {
+    const float mn = warp_sum(mp[hd]), l = warp_sum(lrun[hd]);
+    float4 s = reinterpret_cast<const float4*>(sacc + hd * 128)[lane];
+    s.x += mn;
+    s.y += mn;
+    s.z += mn;
+    s.w += mn;
+    __stcg(reinterpret_cast<float4*>(part + hd * kPartFloats) + lane, s);
+    if (lane == 0) __stcg(reinterpret_cast<float2*>(part + hd * kPartFloats + 128), make_float2(mrun[hd], l));
+    mp[hd] = 0.f;
+    mrun[hd] = kMinusInf;
+    lrun[hd] = 0.f;
+  }
+  __syncwarp();
+  zero_sums<G>(sacc, lane);
+  __syncwarp();
+}
+
+// Resident CTAs per SM the register budget is sized for.
+constexpr int flat_min_ctas(int g) { return g == 1 ? 5 : 0; }
+
+template <int BITS, int G, class Plan>
+__global__ void __launch_bounds__(kWinWarps * 32, flat_min_ctas(G))
+    window_flat_kernel(const WindowArgs a, const __grid_constant__ Plan plan) {
+  using F = FlatCfg<BITS, G>;
+  using L = I8Layout<G>;
+  constexpr int NH = L::kNH;
+  extern __shared__ __align__(128) unsigned char smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int warp = blockIdx.x * kWinWarps + (threadIdx.x >> 5);
+  if (warp >= a.n_warps) return;
+  const FlatMem<BITS, G> m{smem + (threadIdx.x >> 5) * F::kWarpSmem};
+  const long lo = (long)((long long)a.n_items * warp / a.n_warps);
+  const long hi = (long)((long long)a.n_items * (warp + 1) / a.n_warps);
+  const int chunks = a.rows / G, rpc = a.kv_heads * chunks;
+  if (lane == 0) {
+    mbar_init(m.bar(0), 1);
+    mbar_init(m.bar(1), 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  // lane 0 and 1 load the K and V entry of an item ({0, 0} for a piece of the tail)
+  auto load_entry = [&](const FlatCursor& c) {
+    const int j = c.i < c.items.front ? c.i : c.items.from + (c.i - c.items.front);
+    uint2 e = make_uint2(0u, 0u);
+    if (lane < 2 && j < c.items.nb) {
+      const int bh = (int)(c.bhc / chunks), b = bh / a.kv_heads;
+      const long at = entry_of(a, b, bh - b * a.kv_heads, j);
+      e = at < 0 ? make_uint2(0xFFFFFFFFu, 0u)
+                 : *reinterpret_cast<const uint2*>((lane == 0 ? a.k_index : a.v_index) + at * 2);
+    }
+    return e;
+  };
+  // lane s issues its record (K: s = 0, V: s = 1)
+  auto issue = [&](int s, bool tail, uint2 e) {
+    if (lane == s) {
+      const int kind = tail ? kKindTail : entry_kind<BITS>(a, e);
+      fence_async_smem();
+      if (kind == kKindRaw || kind == kKindPacked) {
+        mbar_arrive_expect_tx(m.bar(s), e.y * 16u);
+        bulk_g2s(m.stage(), (s ? a.v_arena : a.k_arena) + (uint64_t)e.x * 16, e.y * 16u, m.bar(s));
+      } else {
+        mbar_arrive(m.bar(s));
+      }
+    }
+    __syncwarp();
+  };
+  FlatCursor cc = flat_at(a, plan, rpc, lo);
+  uint2 ent = load_entry(cc);
+  auto is_tail = [](const FlatCursor& c) { return c.i >= c.items.front + (c.items.nb - c.items.from); };
+  issue(0, is_tail(cc), ent);
+
+  float qr[G][4], mrun[G], lrun[G], mp[G];
+  float acc_lo[NH][8], acc_hi[NH][8];
+#pragma unroll
+  for (int hd = 0; hd < G; ++hd) {
+    mrun[hd] = kMinusInf;
+    lrun[hd] = 0.f;
+    mp[hd] = 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < NH; ++j)
+#pragma unroll
+    for (int T8 = 0; T8 < 8; ++T8) acc_lo[j][T8] = acc_hi[j][T8] = 0.f;
+  float* sacc = m.sums();
+  float* sc = m.scores();
+  zero_sums<G>(sacc, lane);
+  __syncwarp();
+  long cur = -1;
+  uint32_t phase = 0u;
+  const int t = lane & 3;
+#pragma unroll 1
+  for (long x = lo; x < hi; ++x, phase ^= 1u) {
+    const int bh = (int)(cc.bhc / chunks), chunk = (int)(cc.bhc - (long)bh * chunks);
+    const int b = bh / a.kv_heads, h = bh - b * a.kv_heads;
+    const uint16_t* qrow = a.q + ((size_t)bh * a.rows + (size_t)chunk * G) * 128;
+    if (cc.bhc != cur) {
+      if (cur >= 0) flat_flush<G>(a, cur, warp, sacc, acc_lo, acc_hi, mp, mrun, lrun, lane);
+      cur = cc.bhc;
+#pragma unroll
+      for (int hd = 0; hd < G; ++hd) {
+        const uint2 v = *reinterpret_cast<const uint2*>(qrow + hd * 128 + 4 * lane);
+        const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+        const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+        qr[hd][0] = u.x;
+        qr[hd][1] = u.y;
+        qr[hd][2] = w.x;
+        qr[hd][3] = w.y;
+      }
+    }
+    const bool tail = is_tail(cc);
+    const int j = cc.i < cc.items.front ? cc.i : cc.items.from + (cc.i - cc.items.front);
+    const int piece = tail ? j - cc.items.nb : 0;
+    const int n_tok = tail ? min(kTailPiece, cc.items.tl - piece * kTailPiece) : 128;
+    const size_t tail_at = ((size_t)bh * 128 + piece * kTailPiece) * 128;
+    const long long pos0 = tail ? (long long)cc.items.nb * 128 + piece * kTailPiece : (long long)j * 128;
+    const long long p0 = (long long)cc.items.nb * 128 + cc.items.tl - a.queries;
+    const bool whole = !tail && seen_of(p0, pos0, a.window, a.sinks).hi >= 127 &&
+                       seen_of(p0 + a.queries - 1, pos0, a.window, a.sinks).all();
+    uint32_t slots = 0x03020100u + 0x04040404u * (uint32_t)lane;  // this lane's four slots' tokens
+    if (!tail && !whole && a.perm != nullptr) {
+      const long at = entry_of(a, b, h, j);
+      if (at >= 0) slots = reinterpret_cast<const uint32_t*>(a.perm + at * 128)[lane];
+    }
+    FlatCursor nc = cc;
+    flat_next(a, plan, rpc, nc);
+    const uint2 ent_next = x + 1 < hi ? load_entry(nc) : make_uint2(0u, 0u);
+    const int len_k = (int)__shfl_sync(0xffffffffu, ent.y, 0), len_v = (int)__shfl_sync(0xffffffffu, ent.y, 1);
+    const int kind_of_lane = entry_kind<BITS>(a, ent);
+    const int kind_k = __shfl_sync(0xffffffffu, kind_of_lane, 0), kind_v = __shfl_sync(0xffffffffu, kind_of_lane, 1);
+
+    // ---- scores ----
+    if (!mbar_wait_bounded(m.bar(0), phase, a.ctrl)) return;  // never landed (status set); nothing else in flight
+    bool ok = true;
+    if (tail)
+      flat_tail_scores<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
+    else if (kind_k == kKindInvalid)
+      ok = false;
+    else
+      ok = record_scores<BITS, G>(m.stage(), kind_k | (len_k << 8), m.table(), qr, sc, a.scale, lane);
+    __syncwarp();
+    issue(1, tail, ent);
+
+    // ---- masks and the running softmax ----
+    float pr[G][4];
+#pragma unroll
+    for (int hd = 0; hd < G; ++hd) {
+      float sv[4];
+      float bm = kMinusInf;
+      const float4 s4 = *reinterpret_cast<const float4*>(sc + hd * 128 + 4 * lane);
+      const float ss[4] = {s4.x, s4.y, s4.z, s4.w};
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sv[i] = ok ? ss[i] : kMinusInf;
+      } else {
+        const Seen see = seen_of(p0 + (chunk * G + hd) / a.group, pos0, a.window, a.sinks);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = (int)((slots >> (8 * i)) & 0xFFu);
+          sv[i] = ok && see(r) && (!tail || r < n_tok) ? ss[i] : kMinusInf;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bm = fmaxf(bm, sv[i]);
+      bm = warp_max(bm);
+      const float m_new = fmaxf(mrun[hd], bm);
+      float ps = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pr[hd][i] = sv[i] == kMinusInf ? 0.f : exp2f((sv[i] - m_new) * kWinLog2e);
+        ps += pr[hd][i];
+      }
+      if (m_new > mrun[hd]) {  // warp-uniform: rescale what was summed under the old maximum
+        const float alpha = mrun[hd] == kMinusInf ? 0.f : exp2f((mrun[hd] - m_new) * kWinLog2e);
+        lrun[hd] *= alpha;
+        mp[hd] *= alpha;
+        if (mrun[hd] != kMinusInf) {
+          float4* row = reinterpret_cast<float4*>(sacc + hd * 128) + lane;
+          const float4 r4 = *row;
+          *row = make_float4(r4.x * alpha, r4.y * alpha, r4.z * alpha, r4.w * alpha);
+#pragma unroll
+          for (int jn = 0; jn < NH; ++jn) {
+            if (L::head(jn, t) == hd) {
+#pragma unroll
+              for (int T8 = 0; T8 < 8; ++T8) {
+                acc_lo[jn][T8] *= alpha;
+                acc_hi[jn][T8] *= alpha;
+              }
+            }
+          }
+        }
+        mrun[hd] = m_new;
+      }
+      lrun[hd] += ps;  // of this lane's slots; summed over the warp at the flush
+    }
+
+    // ---- values ----
+    if (!mbar_wait_bounded(m.bar(1), phase, a.ctrl)) return;
+    if (tail) {
+      __syncwarp();
+#pragma unroll
+      for (int hd = 0; hd < G; ++hd)
+        *reinterpret_cast<float4*>(sc + hd * 128 + 4 * lane) = make_float4(pr[hd][0], pr[hd][1], pr[hd][2], pr[hd][3]);
+      __syncwarp();
+      flat_tail_values<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
+    } else if (kind_v == kKindInvalid) {
+      ok = false;
+    } else if (ok) {
+      ok = record_values<BITS, G>(m.stage(), kind_v | (len_v << 8), m.table(), pr, acc_lo, acc_hi, sacc, mp, lane);
+    }
+    if (!ok && lane == 0) set_status(a.ctrl, PACKKV_DEV_BAD_RECORD);
+    __syncwarp();
+    if (x + 1 < hi) issue(0, is_tail(nc), ent_next);
+    cc = nc;
+    ent = ent_next;
+  }
+  if (cur >= 0) flat_flush<G>(a, cur, warp, sacc, acc_lo, acc_hi, mp, mrun, lrun, lane);
+}
+
+// Joins the slots of every output row with the log-sum-exp rule in a fixed order: one CTA
+// of four warps per row, warp i takes slots w0 + i, w0 + i + 4, ...
+template <class Plan>
+__global__ void __launch_bounds__(128) window_merge_kernel(const WindowArgs a, int group, const __grid_constant__ Plan plan) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float4 wsum[4][32];
+  __shared__ float2 wml[4];
+  const int chunks = a.rows / group, rpc = a.kv_heads * chunks;
+  const long row = blockIdx.x;  // of out
+  const long bhc = row / group;
+  const int hd = (int)(row - bhc * group), b = (int)(bhc / rpc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const ItemList items = row_list(a, plan, b);
+  float4* out = reinterpret_cast<float4*>(a.out + row * 128) + lane;
+  if (items.n == 0) {  // a sequence without tokens
+    if (warp == 0) *out = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  long first;
+  if constexpr (std::is_same<Plan, WindowPlan>::value)
+    first = plan.base[b] + (bhc - (long)b * rpc) * items.n;
+  else
+    first = bhc * items.n;
+  // warp whose range [w*N/W, (w+1)*N/W) holds an item
+  auto warp_of = [&](long item) { return (long)(((long long)(item + 1) * a.n_warps + a.n_items - 1) / a.n_items) - 1; };
+  const long w0 = warp_of(first), w1 = warp_of(first + items.n - 1);
+  const float* base = a.partials + hd * kPartFloats;
+  const size_t stride = (size_t)group * kPartFloats;
+  float M = kMinusInf, l = 0.f;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (long w = w0 + warp; w <= w1; w += 4) {
+    const float* p = base + (w + bhc) * stride;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + 128));
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(p) + lane);
+    const float m = fmaxf(M, ml.x);
+    const float eo = M == kMinusInf ? 0.f : exp2f((M - m) * kWinLog2e);
+    const float en = ml.y == 0.f ? 0.f : exp2f((ml.x - m) * kWinLog2e);  // 0 sum: nothing was seen
+    if (en != 0.f) {
+      s.x = fmaf(y.x, en, s.x * eo);
+      s.y = fmaf(y.y, en, s.y * eo);
+      s.z = fmaf(y.z, en, s.z * eo);
+      s.w = fmaf(y.w, en, s.w * eo);
+      l = fmaf(ml.y, en, l * eo);
+      M = m;
+    } else if (ml.y != ml.y) {
+      l = ml.y;
+    }
+  }
+  wsum[warp][lane] = s;
+  if (lane == 0) wml[warp] = make_float2(M, l);
+  __syncthreads();
+  if (warp != 0) return;
+  float top = kMinusInf;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = fmaxf(top, wml[i].x);
+  float L = 0.f;
+  s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 ml = wml[i];
+    const float e = ml.y == 0.f ? 0.f : exp2f((ml.x - top) * kWinLog2e);
+    const float4 y = wsum[i][lane];
+    if (e != 0.f) {
+      s.x = fmaf(y.x, e, s.x);
+      s.y = fmaf(y.y, e, s.y);
+      s.z = fmaf(y.z, e, s.z);
+      s.w = fmaf(y.w, e, s.w);
+    }
+    L = fmaf(ml.y, e, L);
+  }
+  *out = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(s.x / L, s.y / L, s.z / L, s.w / L);
+}
+
 struct WinKernel {
   const void* fn;
   int smem;
 };
 
 template <class Plan>
-bool win_select(int bits, int g, WinKernel* k) {
-#define PACKKV_WCASE(B, GG)                                                                                     \
-  if (bits == B && g == GG) {                                                                                   \
-    *k = {reinterpret_cast<const void*>(&window_kernel<B, GG, Plan>), kWinWarps * WinCfg<B, GG>::kWarpSmem};     \
-    return true;                                                                                                \
+bool win_select(int bits, int g, bool flat, WinKernel* k) {
+#define PACKKV_WCASE(B, GG)                                                                                         \
+  if (bits == B && g == GG) {                                                                                       \
+    *k = flat ? WinKernel{reinterpret_cast<const void*>(&window_flat_kernel<B, GG, Plan>),                          \
+                          kWinWarps * FlatCfg<B, GG>::kWarpSmem}                                                    \
+              : WinKernel{reinterpret_cast<const void*>(&window_kernel<B, GG, Plan>), kWinWarps * WinCfg<B, GG>::kWarpSmem}; \
+    return true;                                                                                                    \
   }
   PACKKV_WCASE(4, 1) PACKKV_WCASE(4, 2) PACKKV_WCASE(4, 4) PACKKV_WCASE(4, 8)
   PACKKV_WCASE(3, 1) PACKKV_WCASE(3, 2) PACKKV_WCASE(3, 4) PACKKV_WCASE(3, 8)
@@ -562,10 +1046,14 @@ bool win_select(int bits, int g, WinKernel* k) {
   return false;
 }
 
-// Raises the kernel's shared memory limit once per device and reads the SM count.
-cudaError_t win_configure(const WinKernel& k, int* sms) {
+struct Residency {
+  int sms, warps;  // warps of the kernel that the device holds
+};
+
+// Raises the kernel's shared memory limit once per device; SMs and resident warps.
+cudaError_t win_configure(const WinKernel& k, Residency* r) {
   static std::mutex mu;
-  static std::unordered_map<long long, int> done;
+  static std::unordered_map<long long, Residency> done;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -573,28 +1061,59 @@ cudaError_t win_configure(const WinKernel& k, int* sms) {
   std::lock_guard<std::mutex> lock(mu);
   auto it = done.find(key);
   if (it != done.end()) {
-    *sms = it->second;
+    *r = it->second;
     return cudaSuccess;
   }
   e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  e = cudaDeviceGetAttribute(&r->sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  done[key] = *sms;
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, kWinWarps * 32, k.smem);
+  if (e != cudaSuccess) return e;
+  if (per_sm < 1) return cudaErrorInvalidConfiguration;
+  r->warps = r->sms * per_sm * kWinWarps;
+  done[key] = *r;
   return cudaSuccess;
 }
 
+int max_flat_warps() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms * 32;
+}
+
 template <class Plan>
-cudaError_t launch_window_t(const WindowArgs& a, const Plan& plan, cudaStream_t stream) {
+cudaError_t launch_window_t(WindowArgs a, const Plan& plan, cudaStream_t stream) {
   const int g = a.rows < 8 ? a.rows : 8;
-  WinKernel k{};
-  if (!win_select<Plan>(a.bits, g, &k)) return cudaErrorInvalidValue;
-  int sms = 0;
-  cudaError_t e = win_configure(k, &sms);
-  if (e != cudaSuccess) return e;
   const long row_chunks = (long)a.batch * a.kv_heads * (a.rows / g);
+  WinKernel k{};
+  Residency r{};
+  if (!win_select<Plan>(a.bits, g, true, &k)) return cudaErrorInvalidValue;
+  cudaError_t e = win_configure(k, &r);
+  if (e != cudaSuccess) return e;
+  if (a.n_items >= r.warps) {
+    a.n_warps = r.warps < max_flat_warps() ? r.warps : max_flat_warps();
+    void* args[] = {&a, const_cast<Plan*>(&plan)};
+    e = cudaLaunchKernel(k.fn, dim3((unsigned)((a.n_warps + kWinWarps - 1) / kWinWarps)), dim3(kWinWarps * 32), args,
+                         (size_t)k.smem, stream);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(row_chunks * g));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, &window_merge_kernel<Plan>, a, g, plan);
+  }
+  if (!win_select<Plan>(a.bits, g, false, &k)) return cudaErrorInvalidValue;
+  e = win_configure(k, &r);
+  if (e != cudaSuccess) return e;
   int ranks = 1;
-  while (ranks < 8 && ranks * kWinWarps < a.most_items && row_chunks * ranks * 2 <= 2L * sms) ranks *= 2;
+  while (ranks < 8 && ranks * kWinWarps < a.most_items && row_chunks * ranks * 2 <= 2L * r.sms) ranks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(row_chunks * ranks));
   cfg.blockDim = dim3(kWinWarps * 32);
@@ -607,19 +1126,35 @@ cudaError_t launch_window_t(const WindowArgs& a, const Plan& plan, cudaStream_t 
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  WindowArgs copy = a;
-  void* args[] = {&copy, const_cast<Plan*>(&plan)};
+  void* args[] = {&a, const_cast<Plan*>(&plan)};
   return cudaLaunchKernelExC(&cfg, k.fn, args);
 }
 
 }  // namespace
 
-int window_items(const WindowArgs& a, int nb, int tl) { return item_list(a.queries, a.window, a.sinks, nb, tl).n; }
+size_t window_workspace_bytes(int batch, int kv_heads, int rows) {
+  const int g = rows < 8 ? rows : 8;
+  return ((size_t)max_flat_warps() + (size_t)batch * kv_heads * (rows / g)) * g * kPartFloats * sizeof(float);
+}
 
-size_t window_workspace_bytes(int, int, int) { return 0; }
-
-cudaError_t launch_window(const WindowArgs& a, const LengthPlan* plan, cudaStream_t stream) {
-  return plan ? launch_window_t<LengthPlan>(a, *plan, stream) : launch_window_t<NoPlan>(a, NoPlan{}, stream);
+cudaError_t launch_window(WindowArgs a, WindowPlan* plan, cudaStream_t stream) {
+  const int g = a.rows < 8 ? a.rows : 8;
+  const long rpc = (long)a.kv_heads * (a.rows / g);
+  if (plan == nullptr) {
+    a.most_items = a.row_items = item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len).n;
+    a.n_items = (long)a.batch * rpc * a.row_items;
+    return launch_window_t<NoPlan>(a, NoPlan{}, stream);
+  }
+  a.n_items = 0;
+  for (int b = 0; b < a.batch; ++b) {
+    const int n = item_list(a.queries, a.window, a.sinks, plan->blocks[b], plan->tail[b]).n;
+    if (n > a.most_items) a.most_items = n;
+    plan->base[b] = (int32_t)a.n_items;
+    a.n_items += n * rpc;
+  }
+  if (a.n_items > 0x7fffffffL) return cudaErrorInvalidValue;
+  plan->base[a.batch] = (int32_t)a.n_items;
+  return launch_window_t<WindowPlan>(a, *plan, stream);
 }
 
 }  // namespace packkv

@@ -10,8 +10,10 @@ the `packkv_cache` struct that points into them.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -72,17 +74,6 @@ class RopeStruct(ctypes.Structure):
                 ("reserved0", ctypes.c_uint32), ("turn", ctypes.c_uint64 * 64)]
 
 
-class Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
-
-
-class HeadsStruct(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
-                ("eps", ctypes.c_float), ("q", Rows), ("k", Rows), ("v", Rows), ("q_weight", ctypes.c_void_p),
-                ("k_weight", ctypes.c_void_p)]
-
-
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m decode_gemv_packkv_b200.build`")
@@ -109,13 +100,13 @@ def _load():
         "packkv_append_token_masked": (ctypes.c_int, [P, vp, vp, ctypes.POINTER(ctypes.c_uint8), vp]),
         "packkv_rope_init": (ctypes.c_int, [vp, u32, u32, f64, i32, f64, f64, f64, f64, f32]),
         "packkv_norm_rope": (ctypes.c_int, [vp, vp, i32, i32, vp, i64, vp, vp, vp, vp]),
-        "packkv_append_norm_rope": (ctypes.c_int, [P, vp, vp, vp, vp, vp]),
+        "packkv_append_norm_rope": (ctypes.c_int, [vp, vp, vp, vp, vp, vp]),
         "packkv_attention_window_workspace_bytes": (sz, [P, i32]),
-        "packkv_attention_window": (ctypes.c_int, [P, vp, i32, i32, i32, i32, f32, vp, vp, sz, vp]),
-        "packkv_fork_sequences": (ctypes.c_int, [P, vp, vp, i32, vp]),
-        "packkv_free_blocks": (ctypes.c_int, [P, vp, vp, vp]),
+        "packkv_attention_window": (ctypes.c_int, [vp, vp, i32, i32, i32, i32, f32, vp, vp, sz, vp]),
+        "packkv_fork_sequences": (ctypes.c_int, [vp, vp, vp, i32, vp]),
+        "packkv_free_blocks": (ctypes.c_int, [vp, vp, vp, vp]),
         "packkv_compact_workspace_bytes": (sz, [P]),
-        "packkv_compact": (ctypes.c_int, [P, P, vp, sz, vp]),
+        "packkv_compact": (ctypes.c_int, [vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -175,6 +166,7 @@ class PackKVCache:
         self.perm = (torch.zeros((batch, kv_heads, max_blocks, BLOCK_TOKENS), dtype=torch.uint8, device=dev)
                      if keep_perm else None)
         self.s = CacheStruct()
+        self.addr = ctypes.addressof(self.s)
         self.s.fmt = Format(FORMAT_VERSION, bits, BLOCK_TOKENS, 32, HEAD_DIM, reorder_key, unit_mode)
         self.s.batch, self.s.kv_heads, self.s.max_blocks = batch, kv_heads, max_blocks
         self.s.n_blocks = self.s.tail_len = 0
@@ -391,62 +383,77 @@ class Rope:
                                                          original_tokens, low, high, amplitude))
 
 
-def _heads(rope, q, k, v, q_weight, k_weight, eps, dims):
-    """The packkv_heads of q, k, v: CUDA tensors of `dims` dimensions ([batch, tokens, heads,
-    128] or [batch, heads, 128]) and any strides, channels contiguous."""
-    some = q if q is not None else k
-    if some is None or (k is None) != (v is None):
+# packkv_heads: dtype, q_heads, kv_heads, eps, the rows of q, k, v, q_weight, k_weight
+_HEADS = struct.Struct("=iiif QqqqQqqqQqqq QQ")
+_NO_ROWS = (0, 0, 0, 0)
+
+
+def _rows(name, x, like, dims):
+    """The packkv_rows of a [batch, tokens, heads, 128] (or [batch, heads, 128]) tensor."""
+    if x is None:
+        return _NO_ROWS
+    shape, stride = x.shape, x.stride()
+    if len(shape) != dims or shape[-1] != HEAD_DIM or stride[-1] != 1:
+        raise ValueError(f"{name} must have {dims} dimensions, the last one {HEAD_DIM} contiguous channels")
+    if x is not like and (shape[:-2] != like.shape[:-2] or x.dtype != like.dtype or x.get_device() != like.get_device()):
+        raise ValueError(f"{name} must have the batch, tokens, dtype and device of the others")
+    return (x.data_ptr(), stride[0], stride[1] if dims == 4 else 0, stride[-2])
+
+
+def _weight(name, w, x, like):
+    if w is None:
+        return 0
+    if (x is None or w.dtype != torch.float32 or w.shape != (HEAD_DIM,) or w.stride(0) != 1
+            or w.get_device() != like.get_device()):
+        raise ValueError(f"{name} must be a contiguous fp32 [{HEAD_DIM}] on the heads' device, for heads that are given")
+    return w.data_ptr()
+
+
+def _heads(q, k, v, q_weight, k_weight, eps, dims):
+    """The packkv_heads of q, k, v: CUDA tensors of any strides, channels contiguous."""
+    like = q if q is not None else k
+    if like is None or (k is None) != (v is None):
         raise ValueError("expected q, or k and v, or all three")
-    in_ = HeadsStruct()
-    if some.dtype not in DTYPES:
-        raise ValueError("q, k, v must be fp16, bf16 or fp32")
-    in_.dtype = DTYPES[some.dtype]
-    in_.eps = -1.0 if eps is None else eps
-    if eps is not None and not eps >= 0:
+    dtype = DTYPES.get(like.dtype)
+    if dtype is None or not like.is_cuda:
+        raise ValueError("q, k, v must be fp16, bf16 or fp32 CUDA tensors")
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights need eps (a norm)")
+        eps = -1.0
+    elif not eps >= 0:
         raise ValueError("eps must be >= 0 (None: no norm)")
-    if eps is None and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights need eps (a norm)")
-    lead = tuple(some.shape[:dims - 2])
-    for name, x in (("q", q), ("k", k), ("v", v)):
-        if x is None:
-            continue
-        if not x.is_cuda or x.dim() != dims or x.dtype != some.dtype or x.device != some.device:
-            raise ValueError(f"{name} must be a CUDA tensor of {dims} dimensions like the others")
-        shape, stride = x.shape, x.stride()
-        if tuple(shape[:dims - 2]) != lead or shape[-1] != HEAD_DIM or stride[-1] != 1:
-            raise ValueError(f"{name} must end in heads of {HEAD_DIM} contiguous channels, batch and tokens as the others")
-        rows = getattr(in_, name)
-        rows.data = x.data_ptr()
-        rows.batch_stride, rows.head_stride = stride[0], stride[-2]
-        rows.token_stride = stride[1] if dims == 4 else 0
-    if q is not None:
-        in_.q_heads = q.shape[-2]
+    rows = _rows("q", q, like, dims) + _rows("k", k, like, dims) + _rows("v", v, like, dims)
+    hk = 0
     if k is not None:
-        in_.kv_heads = k.shape[-2]
-        if v.shape[-2] != in_.kv_heads:
+        hk = k.shape[-2]
+        if v.shape[-2] != hk:
             raise ValueError("k and v must have the same heads")
-    for name, w, x in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
-        if w is None:
-            continue
-        if (x is None or w.dtype != torch.float32 or tuple(w.shape) != (HEAD_DIM,) or not w.is_contiguous()
-                or w.device != some.device):
-            raise ValueError(f"{name} must be a contiguous fp32 [{HEAD_DIM}] on the heads' device")
-        setattr(in_, name, w.data_ptr())
-    return in_, some
+    return _HEADS.pack(dtype, 0 if q is None else q.shape[-2], hk, eps, *rows, _weight("q_weight", q_weight, q, like),
+                       _weight("k_weight", k_weight, k, like)), like
 
 
-def _on_device(t: torch.Tensor, stream):
-    """The stream a call for tensors like t goes to: `stream`, or the current one of t's
-    device.  The launch itself goes to the current device, which must be t's."""
-    if t.device.index != torch.cuda.current_device():
+def _stream_of(t: torch.Tensor, stream):
+    """The stream a call for tensors like t goes to: `stream`, or the current one.  The
+    launch goes to the current device, which must be t's."""
+    at = t.get_device()
+    if at != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    # the raw handle; torch.cuda.current_stream() would wrap it in an object first
+    return torch._C._cuda_getCurrentRawStream(at) if stream is None else stream.cuda_stream
 
 
-def _fp16_out(name, out, shape, device):
-    if out is None or out.dtype != torch.float16 or tuple(out.shape) != shape or out.device != device:
-        raise ValueError(f"{name} must be fp16 {shape} on the inputs' device")
-    return _ptr(out)
+def _out_ptr(name, out, dtype, shape, at):
+    """A contiguous output's address."""
+    if out is None or out.dtype != dtype or out.shape != shape or out.get_device() != at or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} on the inputs' device")
+    return out.data_ptr()
+
+
+def _int32s(values):
+    """A host int32 array and its address (keep the array until the call has returned)."""
+    a = array.array("i", values)
+    return a, a.buffer_info()[0]
 
 
 def packkv_norm_rope(rope: Rope | None, q, k, v, q_out=None, k_out=None, v_out=None, q_weight=None, k_weight=None,
@@ -454,15 +461,21 @@ def packkv_norm_rope(rope: Rope | None, q, k, v, q_out=None, k_out=None, v_out=N
     """Norm (eps given) and rotation (rope given) of q, k [batch, tokens, heads, 128], v cast,
     into q_out, k_out, v_out: fp16 [batch, heads, tokens, 128].  q, or k and v, may be None.
     Positions: int32 [batch, tokens], or first + t."""
-    in_, some = _heads(rope, q, k, v, q_weight, k_weight, eps, 4)
-    B, T = some.shape[0], some.shape[1]
-    ptrs = [None if x is None else _fp16_out(name, out, (B, x.shape[2], T, HEAD_DIM), some.device)
+    heads, like = _heads(q, k, v, q_weight, k_weight, eps, 4)
+    B, T = like.shape[0], like.shape[1]
+    at = like.get_device()
+    ptrs = [None if x is None else _out_ptr(name, out, torch.float16, (B, x.shape[2], T, HEAD_DIM), at)
             for name, x, out in (("q_out", q, q_out), ("k_out", k, k_out), ("v_out", v, v_out))]
-    if positions is not None and (positions.dtype != torch.int32 or tuple(positions.shape) != (B, T)
-                                  or positions.device != some.device):
-        raise ValueError(f"positions must be int32 {(B, T)} on the inputs' device")
-    _check("packkv_norm_rope", _lib.packkv_norm_rope(rope.ref if rope is not None else None, ctypes.byref(in_), B, T,
-                                                     _ptr(positions), first, *ptrs, _on_device(some, stream)))
+    pos = None
+    if positions is not None:
+        if (positions.dtype != torch.int32 or positions.shape != (B, T) or positions.get_device() != at
+                or not positions.is_contiguous()):
+            raise ValueError(f"positions must be a contiguous int32 {(B, T)} on the inputs' device")
+        pos = positions.data_ptr()
+    status = _lib.packkv_norm_rope(None if rope is None else rope.ref, heads, B, T, pos, first, *ptrs,
+                                   _stream_of(like, stream))
+    if status:
+        _check("packkv_norm_rope", status)
 
 
 def packkv_append_norm_rope(cache: PackKVCache, rope: Rope | None, q, k, v, q_out=None, q_weight=None, k_weight=None,
@@ -470,18 +483,19 @@ def packkv_append_norm_rope(cache: PackKVCache, rope: Rope | None, q, k, v, q_ou
     """One token per sequence, q, k, v [batch, heads, 128]: norm and rotation at the position
     the cache gives it, k and v appended, q to q_out (fp16 [batch, q_heads, 128]).  active:
     as for packkv_append_token_masked (ragged caches), None for all."""
-    in_, some = _heads(rope, q, k, v, q_weight, k_weight, eps, 3)
-    if k is None or k.shape[0] != cache.s.batch or k.shape[1] != cache.s.kv_heads or k.device != cache.k_tail.device:
+    heads, like = _heads(q, k, v, q_weight, k_weight, eps, 3)
+    at, batch = like.get_device(), cache.s.batch
+    if k is None or k.shape[0] != batch or k.shape[1] != cache.s.kv_heads or at != cache.k_tail.get_device():
         raise ValueError("k, v must be [batch, kv_heads, 128] on the cache's device")
-    qp = None if q is None else _fp16_out("q_out", q_out, tuple(q.shape), some.device)
-    act = None
+    qp = None if q is None else _out_ptr("q_out", q_out, torch.float16, q.shape, at)
     if active is not None:
-        if len(active) != cache.s.batch:
+        active = bytes(map(bool, active))
+        if len(active) != batch:
             raise ValueError("active needs an entry for every sequence")
-        act = (ctypes.c_uint8 * cache.s.batch)(*[1 if x else 0 for x in active])
-    _check("packkv_append_norm_rope", _lib.packkv_append_norm_rope(
-        ctypes.byref(cache.s), rope.ref if rope is not None else None, ctypes.byref(in_), act, qp,
-        _on_device(some, stream)))
+    status = _lib.packkv_append_norm_rope(cache.addr, None if rope is None else rope.ref, heads, active, qp,
+                                          _stream_of(like, stream))
+    if status:
+        _check("packkv_append_norm_rope", status)
 
 
 def packkv_attention_window(cache: PackKVCache, q: torch.Tensor, scale: float, out: torch.Tensor, window: int,
@@ -490,34 +504,44 @@ def packkv_attention_window(cache: PackKVCache, q: torch.Tensor, scale: float, o
     `sinks`: q fp16 [batch, q_heads, 128] with q_heads = kv_heads * queries * G, row
     (h * queries + s) * G + g; out fp32 of the same shape.  The cache keeps its
     permutations (keep_perm=True) unless it does not reorder."""
-    if (q.dtype != torch.float16 or q.dim() != 3 or q.shape[0] != cache.s.batch or q.shape[2] != HEAD_DIM
-            or out.dtype != torch.float32 or out.shape != q.shape or q.device != cache.k_tail.device
-            or out.device != q.device):
-        raise ValueError("q must be fp16 and out fp32 [batch, q_heads, 128], on the cache's device")
+    shape, at = q.shape, cache.k_tail.get_device()
+    if len(shape) != 3 or shape[0] != cache.s.batch or shape[2] != HEAD_DIM:
+        raise ValueError("q must be fp16 [batch, q_heads, 128] on the cache's device")
     if ws is None:
-        ws = cache.window_workspace(q.shape[1])
-    _check("packkv_attention_window", _lib.packkv_attention_window(
-        ctypes.byref(cache.s), _ptr(q), q.shape[1], queries, window, sinks, scale, _ptr(out), _ptr(ws), ws.numel(),
-        _on_device(q, stream)))
+        ws = cache.window_workspace(shape[1])
+    status = _lib.packkv_attention_window(cache.addr, _out_ptr("q", q, torch.float16, shape, at), shape[1], queries,
+                                          window, sinks, scale, _out_ptr("out", out, torch.float32, shape, at),
+                                          _ws_ptr(ws, at), ws.nbytes, _stream_of(q, stream))
+    if status:
+        _check("packkv_attention_window", status)
+
+
+def _ws_ptr(ws, at):
+    if ws.get_device() != at or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the cache's device")
+    return ws.data_ptr()
 
 
 def packkv_fork_sequences(cache: PackKVCache, src, dst, stream=None):
     """Sequence dst[i] becomes a copy of sequence src[i] (lists of sequence numbers)."""
-    n = len(src)
-    if len(dst) != n:
+    a, ap = _int32s(src)
+    b, bp = _int32s(dst)
+    if len(a) != len(b):
         raise ValueError("src and dst must have the same length")
-    arr = ctypes.c_int32 * n
-    _check("packkv_fork_sequences", _lib.packkv_fork_sequences(ctypes.byref(cache.s), arr(*src), arr(*dst), n,
-                                                               _on_device(cache.k_tail, stream)))
+    status = _lib.packkv_fork_sequences(cache.addr, ap, bp, len(a), _stream_of(cache.k_tail, stream))
+    if status:
+        _check("packkv_fork_sequences", status)
 
 
 def packkv_free_blocks(cache: PackKVCache, first, count, stream=None):
     """Gives up blocks first[b] .. first[b] + count[b] - 1 of every sequence (lists of ints)."""
-    if len(first) != cache.s.batch or len(count) != cache.s.batch:
+    a, ap = _int32s(first)
+    b, bp = _int32s(count)
+    if len(a) != cache.s.batch or len(b) != cache.s.batch:
         raise ValueError("first and count need an entry for every sequence")
-    arr = ctypes.c_int32 * cache.s.batch
-    _check("packkv_free_blocks", _lib.packkv_free_blocks(ctypes.byref(cache.s), arr(*first), arr(*count),
-                                                         _on_device(cache.k_tail, stream)))
+    status = _lib.packkv_free_blocks(cache.addr, ap, bp, _stream_of(cache.k_tail, stream))
+    if status:
+        _check("packkv_free_blocks", status)
 
 
 def packkv_compact_workspace_bytes(cache: PackKVCache) -> int:
@@ -526,12 +550,14 @@ def packkv_compact_workspace_bytes(cache: PackKVCache) -> int:
 
 def packkv_compact(dst: PackKVCache, src: PackKVCache, ws: torch.Tensor | None = None, stream=None):
     """Copies what src holds into dst, its live records packed from the start of dst's arenas."""
-    if dst.k_arena.device != src.k_arena.device:
+    at = src.k_arena.get_device()
+    if dst.k_arena.get_device() != at:
         raise ValueError("both caches must be on one device")
     if ws is None:
         ws = src.compact_workspace()
-    _check("packkv_compact", _lib.packkv_compact(ctypes.byref(dst.s), ctypes.byref(src.s), _ptr(ws), ws.numel(),
-                                                 _on_device(src.k_arena, stream)))
+    status = _lib.packkv_compact(dst.addr, src.addr, _ws_ptr(ws, at), ws.nbytes, _stream_of(src.k_arena, stream))
+    if status:
+        _check("packkv_compact", status)
 
 
 def packkv_get_status(cache: PackKVCache, stream=None) -> int:

@@ -34,24 +34,18 @@ def test_rope_init(pk):
 
 
 def _heads(pk, **over):
-    h = pk.HeadsStruct()
-    h.dtype, h.q_heads, h.kv_heads, h.eps = 0, 4, 2, -1.0
-    for name, n in (("q", 4), ("k", 2), ("v", 2)):
-        rows = getattr(h, name)
-        rows.data, rows.batch_stride, rows.token_stride, rows.head_stride = 0x30000000, 1024, 1024, 128
-    for k, v in over.items():
-        if k in ("q", "k", "v"):
-            getattr(h, k).data = v
-        else:
-            setattr(h, k, v)
-    return h
+    """A packkv_heads of fp16 rows (q 4 heads, k and v 2), fields replaced by name."""
+    f = dict(dtype=0, q_heads=4, kv_heads=2, eps=-1.0, q=0x30000000, k=0x30000000, v=0x30000000, q_weight=0, k_weight=0)
+    f.update(over)
+    rows = [x for name in "qkv" for x in (f[name], 1024, 1024, 128)]
+    return pk._HEADS.pack(f["dtype"], f["q_heads"], f["kv_heads"], f["eps"], *rows, f["q_weight"], f["k_weight"])
 
 
 def test_norm_rope_refusals(pk):
     call = pk._lib.packkv_norm_rope
 
     def run(h, batch=1, tokens=1, positions=None, q=X, k=X, v=X, rope=None):
-        return call(rope, ctypes.byref(h), batch, tokens, positions, 0, q, k, v, None)
+        return call(rope, h, batch, tokens, positions, 0, q, k, v, None)
 
     bad = pk.ERR_INVALID_ARG
     assert run(_heads(pk), batch=0) == pk.OK and run(_heads(pk), tokens=0) == pk.OK
@@ -78,20 +72,20 @@ def test_append_norm_rope_refusals(pk):
     call = pk._lib.packkv_append_norm_rope
     s = _fake_cache(pk)
     act = (ctypes.c_uint8 * 2)(1, 1)
-    assert call(ctypes.byref(s), None, ctypes.byref(_heads(pk, kv_heads=3)), None, X, None) == pk.ERR_INVALID_ARG
-    assert call(ctypes.byref(s), None, ctypes.byref(_heads(pk, k=0, v=0)), None, X, None) == pk.ERR_INVALID_ARG
-    assert call(ctypes.byref(s), None, ctypes.byref(_heads(pk)), None, ODD, None) == pk.ERR_INVALID_ARG
-    assert call(ctypes.byref(s), None, ctypes.byref(_heads(pk)), act, X, None) == pk.ERR_UNSUPPORTED
+    assert call(ctypes.addressof(s), None, (_heads(pk, kv_heads=3)), None, X, None) == pk.ERR_INVALID_ARG
+    assert call(ctypes.addressof(s), None, (_heads(pk, k=0, v=0)), None, X, None) == pk.ERR_INVALID_ARG
+    assert call(ctypes.addressof(s), None, (_heads(pk)), None, ODD, None) == pk.ERR_INVALID_ARG
+    assert call(ctypes.addressof(s), None, (_heads(pk)), act, X, None) == pk.ERR_UNSUPPORTED
     s = _fake_cache(pk, n_blocks=4, tail_len=127)
-    assert call(ctypes.byref(s), None, ctypes.byref(_heads(pk)), None, X, None) == pk.ERR_CAPACITY
+    assert call(ctypes.addressof(s), None, (_heads(pk)), None, X, None) == pk.ERR_CAPACITY
     assert s.n_blocks == 4 and s.tail_len == 127
     P = ctypes.POINTER(ctypes.c_int32)
     blocks, tail = (ctypes.c_int32 * 2)(4, 1), (ctypes.c_int32 * 2)(127, 5)
     s = _fake_cache(pk)
     s.seq_blocks, s.seq_tail = ctypes.cast(blocks, P), ctypes.cast(tail, P)
-    assert call(ctypes.byref(s), None, ctypes.byref(_heads(pk)), None, X, None) == pk.ERR_CAPACITY
+    assert call(ctypes.addressof(s), None, (_heads(pk)), None, X, None) == pk.ERR_CAPACITY
     none = (ctypes.c_uint8 * 2)(0, 0)
-    assert call(ctypes.byref(s), None, ctypes.byref(_heads(pk)), none, X, None) == pk.OK   # no token: nothing runs
+    assert call(ctypes.addressof(s), None, (_heads(pk)), none, X, None) == pk.OK   # no token: nothing runs
     assert list(blocks) == [4, 1] and list(tail) == [127, 5]
 
 
@@ -99,7 +93,7 @@ def test_window_refusals(pk):
     call = pk._lib.packkv_attention_window
 
     def run(s, q=X, q_heads=4, queries=1, window=8, sinks=0, out=X):
-        return call(ctypes.byref(s), q, q_heads, queries, window, sinks, 1.0, out, X, 1 << 40, None)
+        return call(ctypes.addressof(s), q, q_heads, queries, window, sinks, 1.0, out, X, 1 << 40, None)
 
     def cache(**over):
         s = _fake_cache(pk, n_blocks=2, **over)
@@ -128,7 +122,7 @@ def test_block_call_refusals(pk):
     def fork(src, dst, s=None):
         s = s or _fake_cache(pk, n_blocks=2)
         n = len(src)
-        return lib.packkv_fork_sequences(ctypes.byref(s), (ctypes.c_int32 * n)(*src), (ctypes.c_int32 * n)(*dst), n, None)
+        return lib.packkv_fork_sequences(ctypes.addressof(s), (ctypes.c_int32 * n)(*src), (ctypes.c_int32 * n)(*dst), n, None)
 
     assert fork([], []) == pk.OK
     assert fork([0], [0]) == bad and fork([0, 1], [1, 0]) == bad and fork([0, 0], [1, 1]) == bad
@@ -137,15 +131,15 @@ def test_block_call_refusals(pk):
     s = _fake_cache(pk, batch=pk.RAGGED_MAX_BATCH + 1)
     assert fork([0], [1], s) == pk.ERR_UNSUPPORTED
     s = _fake_cache(pk, n_blocks=2)
-    assert lib.packkv_fork_sequences(ctypes.byref(s), None, None, 1, None) == bad
+    assert lib.packkv_fork_sequences(ctypes.addressof(s), None, None, 1, None) == bad
 
     def free(first, count):
-        return lib.packkv_free_blocks(ctypes.byref(s), A(*first), A(*count), None)
+        return lib.packkv_free_blocks(ctypes.addressof(s), A(*first), A(*count), None)
 
     assert free([0, 0], [0, 0]) == pk.OK
     assert free([0, 0], [3, 0]) == bad and free([2, 0], [1, 0]) == bad and free([-1, 0], [1, 0]) == bad
     assert free([0, 0], [0, -1]) == bad and free([1 << 30, 0], [(1 << 31) - 1, 0]) == bad
-    assert lib.packkv_free_blocks(ctypes.byref(s), None, A(0, 0), None) == bad
+    assert lib.packkv_free_blocks(ctypes.addressof(s), None, A(0, 0), None) == bad
 
     def other(**over):
         d = _fake_cache(pk, **over)
@@ -157,7 +151,7 @@ def test_block_call_refusals(pk):
     assert need > 0
 
     def compact(d, ws=X, size=None, src=s):
-        return lib.packkv_compact(ctypes.byref(d), ctypes.byref(src), ws, need if size is None else size, None)
+        return lib.packkv_compact(ctypes.addressof(d), ctypes.addressof(src), ws, need if size is None else size, None)
 
     assert compact(other(bits=3)) == bad and compact(other(batch=1)) == bad and compact(other(kv_heads=1)) == bad
     assert compact(other(max_blocks=1)) == pk.ERR_CAPACITY
