@@ -179,10 +179,9 @@ struct WindowArgs {
   int rows;                 // query rows per kv head: queries * group
   int group, queries, window, sinks;
   int n_blocks, tail_len;   // uniform batches
-  int most_items;           // items of the longest row (set by launch_window, with the next three)
-  int row_items;            // items of every row (uniform batches)
+  int most_items;           // items of the longest row (set by launch_window, with the next two)
   long n_items;             // items of all (row, chunk)s
-  int n_warps;              // warps sharing them
+  int n_parts;              // warps sharing them (the even split)
   const uint16_t* q;        // [batch][kv_heads][rows][128]
   float scale;
   float* out;

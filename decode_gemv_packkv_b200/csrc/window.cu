@@ -8,16 +8,12 @@
 // the first query's window on, and the tail in pieces of 32 tokens.  A block that every
 // query sees whole needs no mask; any other is masked slot by slot through the block's
 // permutation.  Records go through the int8 tensor-core decode of the other products
-// (decode.cuh), the fp16 tail through m16n8k16 (q·k exact products, p as two halves).
-// The running maximum and sum of the softmax, and the value sums, are fp32.
-//
-// A cluster of CTAs serves one row (up to 8 query rows of it): its warps take the items
-// in turn, each with its K and V record in flight together, and the warps' sums are
-// merged through (distributed) shared memory in a fixed order, so the call is one launch
-// and its results do not depend on timing.
+// (decode.cuh), with four digits; the running maximum and sum of the softmax and the value
+// sums are fp32, and neither scores nor probabilities reach global memory.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 #include <unordered_map>
@@ -32,36 +28,13 @@ namespace cg = cooperative_groups;
 
 constexpr int kWinWarps = 4;
 constexpr int kTailPiece = 32;
+constexpr int kMaxRanks = 8;  // CTAs of a cluster
+constexpr float kWinLog2e = 1.4426950408889634f;
+constexpr float kMinusInf = -__builtin_huge_valf();
 // Four digits of q' and p' (decode.cuh): over a long window the values average out, and
 // three digits' score error (2^-22 of the largest q') showed as 1.7e-5 of the output.
 constexpr int kWinDigits = 4;
-constexpr float kWinLog2e = 1.4426950408889634f;
-constexpr float kMinusInf = -__builtin_huge_valf();
-
-template <int BITS, int G>
-struct WinCfg {
-  using C = Cfg<BITS, G, false>;
-  static constexpr int kNT = C::kNT;
-  static constexpr int kStage = C::kStageRec;
-  static constexpr int kTableBytes = (C::kI8Tab + 15) / 16 * 16;
-  static constexpr int kScoreBytes = 512 * G;
-  static constexpr int kSumBytes = 512 * G;
-  static constexpr int kFixed = 2 * kStage + kTableBytes + kScoreBytes + kSumBytes;
-  static constexpr int kWarpSmem = (kFixed + 32 + 127) / 128 * 128;
-};
-
-// Warp-private shared memory: [K stage][V stage][table][scores][sums][2 mbarriers][2 kinds].
-template <int BITS, int G>
-struct WinMem {
-  using W = WinCfg<BITS, G>;
-  unsigned char* base;
-  __device__ unsigned char* stage(int s) const { return base + s * W::kStage; }
-  __device__ uint32_t* table() const { return reinterpret_cast<uint32_t*>(base + 2 * W::kStage); }
-  __device__ float* scores() const { return reinterpret_cast<float*>(base + 2 * W::kStage + W::kTableBytes); }
-  __device__ float* sums() const { return scores() + 128 * G; }
-  __device__ uint64_t* bar(int s) const { return reinterpret_cast<uint64_t*>(base + W::kFixed) + s; }
-  __device__ int* kind(int s) const { return reinterpret_cast<int*>(base + W::kFixed + 16) + s; }
-};
+constexpr int kPartFloats = 132;  // per (slot, query row) of the workspace: 128 sums, maximum, sum of exp, pad
 
 // The items of a row that holds nb blocks and tl tail tokens.
 struct ItemList {
@@ -85,135 +58,6 @@ __host__ __device__ inline ItemList item_list(int queries, int window, int sinks
   return x;
 }
 
-__device__ __forceinline__ int row_blocks(const WindowArgs& a, const NoPlan&, int) { return a.n_blocks; }
-__device__ __forceinline__ int row_blocks(const WindowArgs&, const WindowPlan& p, int b) { return p.blocks[b]; }
-__device__ __forceinline__ int row_tail(const WindowArgs& a, const NoPlan&, int) { return a.tail_len; }
-__device__ __forceinline__ int row_tail(const WindowArgs&, const WindowPlan& p, int b) { return p.tail[b]; }
-
-// What one query row sees, relative to a block's first token.
-__device__ __forceinline__ bool sees(long long pos, long long p, int window, int sinks) {
-  return pos <= p && (pos > p - window || pos < sinks);
-}
-
-// m16n8k16, fp16 operands, fp32 accumulators.
-__device__ __forceinline__ void hmma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Scaled scores of n <= 32 tail tokens (rows of 128 fp16 from `tail`) into sc[head*128 + t].
-// The contraction's channel order is free: lane (g, t) takes channels 32 kk + 8t .. +7 of
-// its token (A) and of its head (B) with one 16-byte load each, two k-steps per load.
-template <int G>
-__device__ __forceinline__ void tail_piece_scores(const uint16_t* tail, const uint16_t* q, int n, float scale,
-                                                  float* sc, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 qb[4];
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk)
-    qb[kk] = g < G ? *reinterpret_cast<const uint4*>(q + (size_t)g * 128 + 32 * kk + 8 * t) : zero;
-#pragma unroll
-  for (int tile = 0; tile < 2; ++tile) {
-    if (16 * tile >= n) break;
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    const int r0 = 16 * tile + g, r1 = r0 + 8;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      const uint4 x = r0 < n ? *reinterpret_cast<const uint4*>(tail + (size_t)r0 * 128 + 32 * kk + 8 * t) : zero;
-      const uint4 y = r1 < n ? *reinterpret_cast<const uint4*>(tail + (size_t)r1 * 128 + 32 * kk + 8 * t) : zero;
-      hmma16816(d, x.x, y.x, x.y, y.y, qb[kk].x, qb[kk].y);
-      hmma16816(d, x.z, y.z, x.w, y.w, qb[kk].z, qb[kk].w);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int head = 2 * t + (i & 1), tok = (i & 2) ? r1 : r0;
-      if (head < G) sc[head * 128 + tok] = scale * d[i];
-    }
-  }
-}
-
-// Adds sum_t p[head][t] v[t][c] of n <= 32 tail tokens into the channel sums (p: fp32 in
-// sc[head*128 + t], zero from n to 31).  p = hi + lo/4096 with fp16 hi, lo (abs. error
-// below 2^-35): rows g of the A tile carry hi, rows g + 8 lo, so one product sums both.
-// Column n of n-tile j is channel 16n + j: lane (g, t) reads 16 channels of its tokens.
-// With an infinity or NaN among the values the tokens are added one by one, those of zero
-// weight left out.
-template <int G>
-__device__ __forceinline__ void tail_piece_values(const uint16_t* tail, const float* sc, int n, float* sacc,
-                                                  int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  float d[16][4];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
-  uint32_t wild = 0u;
-#pragma unroll
-  for (int tile = 0; tile < 2; ++tile) {
-    if (16 * tile >= n) break;
-    uint32_t a[4];  // rows g (hi): k 2t, 2t+1 | rows g + 8 (lo) | k + 8
-#pragma unroll
-    for (int kh = 0; kh < 2; ++kh) {
-      const int k = 16 * tile + 2 * t + 8 * kh;
-      const float p0 = g < G ? sc[g * 128 + k] : 0.f, p1 = g < G ? sc[g * 128 + k + 1] : 0.f;
-      const __half2 hi = __floats2half2_rn(p0, p1);
-      const float2 hf = __half22float2(hi);
-      const __half2 lo = __floats2half2_rn((p0 - hf.x) * 4096.f, (p1 - hf.y) * 4096.f);
-      a[2 * kh] = *reinterpret_cast<const uint32_t*>(&hi);
-      a[2 * kh + 1] = *reinterpret_cast<const uint32_t*>(&lo);
-    }
-    uint4 v[4][2];  // tokens 2t, 2t+1, 2t+8, 2t+9 of the tile, channels 16g .. 16g+15
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int tok = 16 * tile + 2 * t + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        v[i][x] = tok < n ? *reinterpret_cast<const uint4*>(tail + (size_t)tok * 128 + 16 * g + 8 * x)
-                          : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {v[i][x].x, v[i][x].y, v[i][x].z, v[i][x].w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {  // an exponent of all ones in either half
-          wild |= ((w[y] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4& q4 = v[i][j >> 3];
-        const int word = (j >> 1) & 3;
-        w[i] = word == 0 ? q4.x : (word == 1 ? q4.y : (word == 2 ? q4.z : q4.w));
-      }
-      const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-      hmma16816(d[j], a[0], a[1], a[2], a[3], __byte_perm(w[0], w[1], sel), __byte_perm(w[2], w[3], sel));
-    }
-  }
-  if (__any_sync(0xffffffffu, wild != 0u)) {
-#pragma unroll 1
-    for (int hd = 0; hd < G; ++hd)
-#pragma unroll 1
-      for (int sl = 0; sl < 4; ++sl) {
-        float s = 0.f;
-        for (int tok = 0; tok < n; ++tok) {
-          const float p = sc[hd * 128 + tok];
-          if (p != 0.f) s = fmaf(p, half_bits_to_float(tail[(size_t)tok * 128 + sl * 32 + lane]), s);
-        }
-        sacc[hd * 128 + sl * 32 + lane] += s;
-      }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)  // rows g: columns 2t, 2t + 1; their lo parts sit in rows g + 8
-        if (g < G) sacc[g * 128 + 16 * (2 * t + i) + j] += fmaf(d[j][2 + i], 1.f / 4096.f, d[j][i]);
-  }
-  __syncwarp();
-}
-
 // The four parameters of this lane (channels or slots 4*lane ..) at `at` of a record.
 __device__ __forceinline__ float4 param4(const unsigned char* st, int at, int lane) {
   const uint2 v = *reinterpret_cast<const uint2*>(st + at + 8 * lane);
@@ -222,11 +66,112 @@ __device__ __forceinline__ float4 param4(const unsigned char* st, int at, int la
   return make_float4(x.x, x.y, y.x, y.y);
 }
 
+// A place in the list of all items: (sequence, kv head, chunk of 8 query rows), item.
+struct ItemCursor {
+  int b, h, chunk, i;
+  ItemList items;  // of the sequence
+
+  // Index of this (row, chunk): row of q and out / G, workspace slot.
+  __device__ long row(const WindowArgs& a, int chunks) const { return ((long)b * a.kv_heads + h) * chunks + chunk; }
+  __device__ int block() const { return i < items.front ? i : items.from + (i - items.front); }  // >= nb: a piece of the tail
+};
+
+__device__ __forceinline__ ItemList row_list(const WindowArgs& a, const NoPlan&, int) {
+  return item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len);
+}
+__device__ __forceinline__ ItemList row_list(const WindowArgs& a, const WindowPlan& p, int b) {
+  return item_list(a.queries, a.window, a.sinks, p.blocks[b], p.tail[b]);
+}
+
+// The cursor at item x of the whole list.
+template <class Plan>
+__device__ __forceinline__ ItemCursor item_at(const WindowArgs& a, const Plan& p, int chunks, long x) {
+  ItemCursor c;
+  const int rpc = a.kv_heads * chunks;  // (row, chunk)s of a sequence
+  if constexpr (std::is_same<Plan, WindowPlan>::value) {
+    int lo = 0, hi = a.batch;  // the last sequence whose first item is <= x has items
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.base[mid] <= x) lo = mid; else hi = mid;
+    }
+    c.b = lo;
+    x -= p.base[lo];
+    c.items = row_list(a, p, lo);
+  } else {
+    c.items = row_list(a, p, 0);
+    const long per = (long)rpc * c.items.n;
+    c.b = (int)(x / per);
+    x -= c.b * per;
+  }
+  const int r = (int)(x / c.items.n);
+  c.i = (int)(x - (long)r * c.items.n);
+  c.h = r / chunks;
+  c.chunk = r - c.h * chunks;
+  return c;
+}
+template <class Plan>
+__device__ __forceinline__ void item_next(const WindowArgs& a, const Plan& p, int chunks, ItemCursor& c) {
+  if (++c.i < c.items.n) return;
+  c.i = 0;
+  if (++c.chunk < chunks) return;
+  c.chunk = 0;
+  if (++c.h < a.kv_heads) return;
+  c.h = 0;
+  ++c.b;
+  if constexpr (std::is_same<Plan, WindowPlan>::value) {  // the next sequence that has items
+    while (c.b < a.batch && p.base[c.b + 1] == p.base[c.b]) ++c.b;
+    if (c.b < a.batch) c.items = row_list(a, p, c.b);
+  }
+}
+
+// Where the index entry and the permutation of a row's logical block j are (-1: the block
+// table names no block).
+__device__ __forceinline__ long entry_of(const WindowArgs& a, int b, int h, int j) {
+  if (a.block_table == nullptr) return ((long)b * a.kv_heads + h) * a.max_blocks + j;
+  const int p = a.block_table[(size_t)b * a.max_blocks + j];
+  if (p < 0 || (long)p >= (long)a.batch * a.max_blocks) return -1;
+  return ((long)(p / a.max_blocks) * a.kv_heads + h) * a.max_blocks + p % a.max_blocks;
+}
+
+// {kind, checked} of an index entry.
+template <int BITS>
+__device__ __forceinline__ int entry_kind(const WindowArgs& a, uint2 e) {
+  constexpr uint32_t raw = (uint32_t)raw_record_bytes(BITS);
+  const bool valid = e.x != 0xFFFFFFFFu && e.y >= 1040 / 16 && e.y * 16u <= raw && (uint64_t)e.x + e.y <= a.arena16;
+  return !valid ? kKindInvalid : (e.y * 16u == raw ? kKindRaw : kKindPacked);
+}
+
+// What a query row sees of the 128 (or fewer) tokens from pos0 on, as bounds on the offset
+// r from pos0: lo < r <= hi, or r < first.
+struct Seen {
+  int lo, hi, first;
+  __device__ bool operator()(int r) const { return r <= hi && (r > lo || r < first); }
+};
+__device__ __forceinline__ int clamp_offset(long long x) { return (int)(x < -1 ? -1 : (x > 128 ? 128 : x)); }
+__device__ __forceinline__ Seen seen_of(long long p, long long pos0, int window, int sinks) {
+  return {clamp_offset(p - window - pos0), clamp_offset(p - pos0), clamp_offset(sinks - pos0)};
+}
+
+// Blocks that every query of a row sees whole: from <= j <= to, or j <= sink with j <= to.
+struct WholeBlocks {
+  int from, to, sink;
+  __device__ bool operator()(int j) const { return j <= to && (j >= from || j <= sink); }
+};
+__device__ __forceinline__ WholeBlocks whole_blocks(const WindowArgs& a, const ItemList& x) {
+  const long long T = (long long)x.nb * 128 + x.tl, p0 = T - a.queries;
+  const long long lo = T - 1 - a.window;  // the last query sees from lo + 1 on
+  WholeBlocks w;
+  w.from = lo < 0 ? 0 : (int)(lo / 128 + 1);
+  w.to = p0 < 127 ? -1 : (int)((p0 - 127) / 128);  // 128 j + 127 <= p0
+  w.sink = a.sinks / 128 - 1;
+  return w;
+}
+
 // Scores of a staged K record into sc; false: the record failed its checks.
 template <int BITS, int G>
 __device__ __forceinline__ bool record_scores(unsigned char* st, int kind_len, uint32_t* tab, const float (&qr)[G][4],
                                               float* sc, float scale, int lane) {
-  constexpr int NT = WinCfg<BITS, G>::kNT;
+  constexpr int NT = I8Layout<G>::kNT;
   const float4 mn = param4(st, kParamOffset, lane), sl = param4(st, kParamOffset + 256, lane);
   float cst[G], qv[G][4], invf[G];
 #pragma unroll
@@ -253,7 +198,7 @@ __device__ __forceinline__ bool record_values(unsigned char* st, int kind_len, u
                                               float (&acc_lo)[I8Layout<G>::kNH][8],
                                               float (&acc_hi)[I8Layout<G>::kNH][8], float* sacc, float (&mp)[G],
                                               int lane) {
-  constexpr int NT = WinCfg<BITS, G>::kNT;
+  constexpr int NT = I8Layout<G>::kNT;
   const float4 mn = param4(st, kParamOffset, lane), sl = param4(st, kParamOffset + 256, lane);
   float pv[G][4], add[G], invf[G];
 #pragma unroll
@@ -275,381 +220,139 @@ __device__ __forceinline__ bool record_values(unsigned char* st, int kind_len, u
   return true;
 }
 
-template <int BITS, int G, class Plan>
-__global__ void __launch_bounds__(kWinWarps * 32) window_kernel(const WindowArgs a,
-                                                                const __grid_constant__ Plan plan) {
-  using W = WinCfg<BITS, G>;
-  using L = I8Layout<G>;
-  constexpr int NH = L::kNH;
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float wmax[kWinWarps][G], wsum[kWinWarps][G], cmax[G], csum[G];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int chunks = a.rows / G;
-  const int rc = blockIdx.x / ranks;
-  const int bh = rc / chunks, chunk = rc - bh * chunks;
-  const int b = bh / a.kv_heads, h = bh - b * a.kv_heads;
-  const WinMem<BITS, G> m{smem + warp * W::kWarpSmem};
-  const ItemList items = item_list(a.queries, a.window, a.sinks, row_blocks(a, plan, b), row_tail(a, plan, b));
-  const long long T = (long long)items.nb * 128 + items.tl;
-  const long long p0 = T - a.queries;  // position of query 0
-  if (lane == 0) {
-    mbar_init(m.bar(0), 1);
-    mbar_init(m.bar(1), 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
+// m16n8k16, fp16 operands, fp32 accumulators.
+__device__ __forceinline__ void hmma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-  // block of item i (>= nb: piece i's tail tokens)
-  auto block_of = [&](int i) { return i < items.front ? i : items.from + (i - items.front); };
-  // issues the K (s = 0) or V (s = 1) record of block j into stage s
-  auto issue = [&](int s, int j) {
-    uint32_t off = 0xFFFFFFFFu, len = 0u;
-    int kind = kKindTail;
-    if (j < items.nb) {
-      size_t at = (size_t)bh * a.max_blocks + j;
-      bool there = true;
-      if (a.block_table != nullptr) {
-        const int p = a.block_table[(size_t)b * a.max_blocks + j];
-        there = p >= 0 && (long)p < (long)a.batch * a.max_blocks;
-        at = there ? ((size_t)(p / a.max_blocks) * a.kv_heads + h) * a.max_blocks + p % a.max_blocks : 0;
-      }
-      if (there) {
-        const uint2 e = *reinterpret_cast<const uint2*>((s ? a.v_index : a.k_index) + at * 2);
-        off = e.x;
-        len = e.y;
-      }
-      const bool valid = off != 0xFFFFFFFFu && len >= 1040 / 16 && len * 16u <= (uint32_t)W::kStage &&
-                         (uint64_t)off + len <= a.arena16;
-      kind = !valid ? kKindInvalid : (len * 16u == (uint32_t)W::kStage ? kKindRaw : kKindPacked);
-    }
-    if (lane == 0) {
-      *m.kind(s) = kind | (int)(len << 8);
-      fence_async_smem();
-      if (kind == kKindRaw || kind == kKindPacked) {
-        mbar_arrive_expect_tx(m.bar(s), len * 16u);
-        bulk_g2s(m.stage(s), (s ? a.v_arena : a.k_arena) + (uint64_t)off * 16, len * 16u, m.bar(s));
-      } else {
-        mbar_arrive(m.bar(s));
-      }
-    }
-    __syncwarp();
-  };
-
-  const int step = ranks * kWinWarps;
-  const int first = rank * kWinWarps + warp;
-  if (first < items.n) {
-    issue(0, block_of(first));
-    issue(1, block_of(first));
-  }
-  const uint16_t* qrow = a.q + ((size_t)bh * a.rows + (size_t)chunk * G) * 128;
-  float qr[G][4], mrun[G], lrun[G], mp[G];
-  float acc_lo[NH][8], acc_hi[NH][8];
-#pragma unroll
-  for (int hd = 0; hd < G; ++hd) {
-    const uint2 v = *reinterpret_cast<const uint2*>(qrow + hd * 128 + 4 * lane);
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
-    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-    qr[hd][0] = x.x;
-    qr[hd][1] = x.y;
-    qr[hd][2] = y.x;
-    qr[hd][3] = y.y;
-    mrun[hd] = kMinusInf;
-    lrun[hd] = 0.f;
-    mp[hd] = 0.f;
-  }
-#pragma unroll
-  for (int j = 0; j < NH; ++j)
-#pragma unroll
-    for (int T8 = 0; T8 < 8; ++T8) acc_lo[j][T8] = acc_hi[j][T8] = 0.f;
-  float* sacc = m.sums();
-  float* sc = m.scores();
-  zero_sums<G>(sacc, lane);
-  __syncwarp();
+// Scaled scores of n <= 32 tail tokens into sc[head*128 + t].  The contraction's channel order is free: lane (g, t) takes
+// channels 32 kk + 8t .. +7 of its token (A) and of its head (B) with one 16-byte load
+// each, two k-steps per load.  Exact products, fp32 sums.
+template <int G>
+__device__ __forceinline__ void tail_scores32(const uint16_t* tail, const uint16_t* q, int n, float scale, float* sc,
+                                              int lane) {
   const int g = lane >> 2, t = lane & 3;
-  uint32_t phase = 0u;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 qb[4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+    qb[kk] = g < G ? *reinterpret_cast<const uint4*>(q + (size_t)g * 128 + 32 * kk + 8 * t) : zero;
+#pragma unroll
+  for (int tile = 0; tile < 2; ++tile) {
+    if (16 * tile >= n) break;
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    const int r0 = 16 * tile + g, r1 = r0 + 8;
+    uint4 x[4], y[4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      x[kk] = r0 < n ? *reinterpret_cast<const uint4*>(tail + (size_t)r0 * 128 + 32 * kk + 8 * t) : zero;
+      y[kk] = r1 < n ? *reinterpret_cast<const uint4*>(tail + (size_t)r1 * 128 + 32 * kk + 8 * t) : zero;
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      hmma16816(d, x[kk].x, y[kk].x, x[kk].y, y[kk].y, qb[kk].x, qb[kk].y);
+      hmma16816(d, x[kk].z, y[kk].z, x[kk].w, y[kk].w, qb[kk].z, qb[kk].w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int head = 2 * t + (i & 1), tok = (i & 2) ? r1 : r0;
+      if (head < G) sc[head * 128 + tok] = scale * d[i];
+    }
+  }
+}
+
+// Adds sum_t p[head][t] v[t][c] over n <= 32 tail tokens into the channel sums (p: fp32 in
+// sc[head*128 + t], zero from n to 31).  p <= 1 = hi + lo/4096 with fp16 hi, lo: rows g
+// of the A tile carry hi, rows g + 8 lo, so one product sums both.  Column m of n-tile j is
+// channel 16m + 8x + j: lane (g, t) reads 8 channels of its tokens per half x.  With an
+// infinity or NaN among the values the tokens are added one by one, those of zero weight
+// (masked ones) left out, so that it does not spread.
+template <int G>
+__device__ __forceinline__ void tail_values32(const uint16_t* tail, const float* sc, int n, float* sacc, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t a[2][4];  // per token tile: rows g (hi) k 2t, 2t+1 | rows g + 8 (lo) | both again for k + 8
+#pragma unroll
+  for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+    for (int kh = 0; kh < 2; ++kh) {
+      const int k = 16 * tile + 2 * t + 8 * kh;
+      const float p0 = g < G ? sc[g * 128 + k] : 0.f, p1 = g < G ? sc[g * 128 + k + 1] : 0.f;
+      const __half2 hi = __floats2half2_rn(p0, p1);
+      const float2 hf = __half22float2(hi);
+      const __half2 lo = __floats2half2_rn((p0 - hf.x) * 4096.f, (p1 - hf.y) * 4096.f);
+      a[tile][2 * kh] = *reinterpret_cast<const uint32_t*>(&hi);
+      a[tile][2 * kh + 1] = *reinterpret_cast<const uint32_t*>(&lo);
+    }
 #pragma unroll 1
-  for (int i = first; i < items.n; i += step, phase ^= 1u) {
-    const int j = block_of(i);
-    const bool more = i + step < items.n;
-    // ---- scores ----
-    if (!mbar_wait_bounded(m.bar(0), phase, a.ctrl)) {  // never landed (status set)
-      mbar_wait_bounded(m.bar(1), phase, a.ctrl);
-      break;
-    }
-    const int kind_k = *m.kind(0);
-    const bool tail = (kind_k & 0xFF) == kKindTail;
-    const int piece = tail ? j - items.nb : 0;
-    const int n_tok = tail ? min(kTailPiece, items.tl - piece * kTailPiece) : 128;
-    const size_t tail_at = ((size_t)bh * 128 + piece * kTailPiece) * 128;
-    bool ok = true;
-    if (tail)
-      tail_piece_scores<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
-    else if ((kind_k & 0xFF) == kKindInvalid)
-      ok = false;
-    else
-      ok = record_scores<BITS, G>(m.stage(0), kind_k, m.table(), qr, sc, a.scale, lane);
-    __syncwarp();
-    if (more) issue(0, block_of(i + step));
-
-    // ---- masks and the running softmax ----
-    const long long pos0 = (long long)j * 128;
-    const bool whole = !tail && pos0 + 127 <= p0 && (pos0 > p0 + a.queries - 1 - a.window || pos0 + 127 < a.sinks);
-    long long pos[4];
+  for (int x = 0; x < 2; ++x) {
+    uint4 v[2][4];  // tokens 2t, 2t+1, 2t+8, 2t+9 of each tile
+    uint32_t ones = 0u;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) pos[x] = pos0 + 4 * lane + x;
-    if (tail) {
+    for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) pos[x] = (long long)items.nb * 128 + piece * kTailPiece + 4 * lane + x;
-    } else if (!whole && a.perm != nullptr) {
-      size_t at = (size_t)bh * a.max_blocks + j;
-      bool there = true;
-      if (a.block_table != nullptr) {
-        const int p = a.block_table[(size_t)b * a.max_blocks + j];
-        there = p >= 0 && (long)p < (long)a.batch * a.max_blocks;
-        at = there ? ((size_t)(p / a.max_blocks) * a.kv_heads + h) * a.max_blocks + p % a.max_blocks : 0;
+      for (int i = 0; i < 4; ++i) {
+        const int tok = 16 * tile + 2 * t + (i & 1) + 8 * (i >> 1);
+        v[tile][i] = tok < n ? *reinterpret_cast<const uint4*>(tail + (size_t)tok * 128 + 16 * g + 8 * x)
+                             : make_uint4(0u, 0u, 0u, 0u);
       }
-      const uint32_t w = there ? reinterpret_cast<const uint32_t*>(a.perm + at * 128)[lane] : 0u;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) pos[x] = pos0 + ((w >> (8 * x)) & 0xFFu);
-    }
-    float pr[G][4];
+    for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
-    for (int hd = 0; hd < G; ++hd) {
-      const long long p = p0 + (chunk * G + hd) / a.group;
-      float sv[4];
-      float bm = kMinusInf;
+      for (int i = 0; i < 4; ++i) {  // an exponent of all ones in either half
+        const uint32_t w[4] = {v[tile][i].x, v[tile][i].y, v[tile][i].z, v[tile][i].w};
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int r = 4 * lane + x;
-        const bool see = ok && r < n_tok && (whole || sees(pos[x], p, a.window, a.sinks));
-        sv[x] = see ? sc[hd * 128 + r] : kMinusInf;
-        bm = fmaxf(bm, sv[x]);
+        for (int y = 0; y < 4; ++y) ones |= ((w[y] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
       }
-      bm = warp_max(bm);
-      const float m_new = fmaxf(mrun[hd], bm);
-      float ps = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        pr[hd][x] = sv[x] == kMinusInf ? 0.f : exp2f((sv[x] - m_new) * kWinLog2e);
-        ps += pr[hd][x];
-      }
-      ps = warp_sum(ps);
-      if (m_new > mrun[hd]) {  // warp-uniform: rescale what was summed under the old maximum
-        const float alpha = mrun[hd] == kMinusInf ? 0.f : exp2f((mrun[hd] - m_new) * kWinLog2e);
-        lrun[hd] *= alpha;
-        mp[hd] *= alpha;
-#pragma unroll
-        for (int sl = 0; sl < 4; ++sl) sacc[hd * 128 + sl * 32 + lane] *= alpha;
-#pragma unroll
-        for (int jn = 0; jn < NH; ++jn) {
-          if (L::head(jn, t) == hd) {
-#pragma unroll
-            for (int T8 = 0; T8 < 8; ++T8) {
-              acc_lo[jn][T8] *= alpha;
-              acc_hi[jn][T8] *= alpha;
-            }
-          }
-        }
-        mrun[hd] = m_new;
-      }
-      lrun[hd] += ps;
-    }
-
-    // ---- values ----
-    if (!mbar_wait_bounded(m.bar(1), phase, a.ctrl)) {
-      if (more) mbar_wait_bounded(m.bar(0), phase ^ 1u, a.ctrl);
-      break;
-    }
-    const int kind_v = *m.kind(1);
-    if (tail) {
-      __syncwarp();
-#pragma unroll
+    if (__any_sync(0xffffffffu, ones != 0u)) {  // these 64 channels (16m + 8x + j) one by one
+#pragma unroll 1
       for (int hd = 0; hd < G; ++hd)
-        *reinterpret_cast<float4*>(sc + hd * 128 + 4 * lane) = make_float4(pr[hd][0], pr[hd][1], pr[hd][2], pr[hd][3]);
-      __syncwarp();
-      tail_piece_values<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
-    } else if ((kind_v & 0xFF) == kKindInvalid) {
-      ok = false;
-    } else if (ok) {
-      ok = record_values<BITS, G>(m.stage(1), kind_v, m.table(), pr, acc_lo, acc_hi, sacc, mp, lane);
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          const int c = 16 * (lane >> 2) + 8 * x + 2 * (lane & 3) + k;
+          float sum = sacc[hd * 128 + c];
+          for (int tok = 0; tok < n; ++tok) {
+            const float p = sc[hd * 128 + tok];
+            if (p != 0.f) sum = fmaf(p, half_bits_to_float(tail[(size_t)tok * 128 + c]), sum);
+          }
+          sacc[hd * 128 + c] = sum;
+        }
+      continue;
     }
-    if (!ok && lane == 0) set_status(a.ctrl, PACKKV_DEV_BAD_RECORD);
-    __syncwarp();
-    if (more) issue(1, block_of(i + step));
-  }
-
-  // ---- this warp's sums, then the CTA's, then the cluster's, each in a fixed order ----
-  __syncwarp();
+    float d[8][4];
 #pragma unroll
-  for (int j = 0; j < NH; ++j) {
-    if (L::owns(j, t)) {
-      float* row = sacc + L::head(j, t) * 128 + g;
+    for (int j = 0; j < 8; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
 #pragma unroll
-      for (int T8 = 0; T8 < 8; ++T8) {
-        row[16 * T8] += acc_lo[j][T8];
-        row[16 * T8 + 8] += acc_hi[j][T8];
+    for (int tile = 0; tile < 2; ++tile)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4& q4 = v[tile][i];
+          w[i] = j < 2 ? q4.x : (j < 4 ? q4.y : (j < 6 ? q4.z : q4.w));
+        }
+        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+        hmma16816(d[j], a[tile][0], a[tile][1], a[tile][2], a[tile][3], __byte_perm(w[0], w[1], sel),
+                  __byte_perm(w[2], w[3], sel));
       }
-    }
-  }
+    if (g < G) {
 #pragma unroll
-  for (int hd = 0; hd < G; ++hd) {
-    const float mn = warp_sum(mp[hd]);
-    __syncwarp();
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-    for (int sl = 0; sl < 4; ++sl) sacc[hd * 128 + sl * 32 + lane] += mn;
-    if (lane == 0) {
-      wmax[warp][hd] = mrun[hd];
-      wsum[warp][hd] = lrun[hd];
+        for (int i = 0; i < 2; ++i)  // columns 2t, 2t + 1; their lo parts sit in rows g + 8
+          sacc[g * 128 + 16 * (2 * t + i) + 8 * x + j] += fmaf(d[j][2 + i], 1.f / 4096.f, d[j][i]);
     }
   }
-  __syncthreads();
-  const WinMem<BITS, G> m0{smem};
-  float* cta = m0.scores();  // [G][128], free now
-  for (int o = threadIdx.x; o < G * 128; o += kWinWarps * 32) {
-    const int hd = o >> 7;
-    float M = wmax[0][hd];
-#pragma unroll
-    for (int w = 1; w < kWinWarps; ++w) M = fmaxf(M, wmax[w][hd]);
-    float s = 0.f, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWinWarps; ++w) {
-      const WinMem<BITS, G> mw{smem + w * W::kWarpSmem};
-      const float e = wsum[w][hd] == 0.f ? 0.f : exp2f((wmax[w][hd] - M) * kWinLog2e);
-      if (e != 0.f) s = fmaf(mw.sums()[o], e, s);
-      l = fmaf(wsum[w][hd], e, l);
-    }
-    cta[o] = s;
-    if ((o & 127) == 0) {
-      cmax[hd] = M;
-      csum[hd] = l;
-    }
-  }
-  if (ranks > 1) cluster.sync(); else __syncthreads();
-  float* orow = a.out + ((size_t)bh * a.rows + (size_t)chunk * G) * 128;
-  for (int o = rank * kWinWarps * 32 + threadIdx.x; o < G * 128; o += ranks * kWinWarps * 32) {
-    const int hd = o >> 7;
-    float M = kMinusInf;
-    for (int r = 0; r < ranks; ++r) M = fmaxf(M, *cluster.map_shared_rank(&cmax[hd], r));
-    float s = 0.f, l = 0.f;
-    for (int r = 0; r < ranks; ++r) {
-      const float lr = *cluster.map_shared_rank(&csum[hd], r);
-      const float e = lr == 0.f ? 0.f : exp2f((*cluster.map_shared_rank(&cmax[hd], r) - M) * kWinLog2e);
-      if (e != 0.f) s = fmaf(*cluster.map_shared_rank(&cta[o], r), e, s);
-      l = fmaf(lr, e, l);
-    }
-    orow[o] = l == 0.f ? 0.f : s / l;  // a row that sees nothing is zero; a NaN stays one
-  }
-  if (ranks > 1) cluster.sync();  // no CTA leaves while another reads its sums
-}
-
-// ---- many items: every resident warp takes a contiguous share ----------------------
-// The items of all (row, chunk)s in one list, split evenly over the warps the device
-// holds.  A warp stages an item's K record, then its V record in the same stage (half
-// the shared memory, so more warps per SM), and at each (row, chunk) border writes its
-// sums to the workspace; window_merge_kernel joins them in a fixed order.
-template <int BITS, int G>
-struct FlatCfg {
-  using C = Cfg<BITS, G, false>;
-  static constexpr int kStage = C::kStageRec;
-  static constexpr int kTableBytes = (C::kI8Tab + 15) / 16 * 16;
-  static constexpr int kFixed = kStage + kTableBytes + 1024 * G;
-  static constexpr int kWarpSmem = (kFixed + 32 + 127) / 128 * 128;
-};
-
-template <int BITS, int G>
-struct FlatMem {
-  using F = FlatCfg<BITS, G>;
-  unsigned char* base;
-  __device__ unsigned char* stage() const { return base; }
-  __device__ uint32_t* table() const { return reinterpret_cast<uint32_t*>(base + F::kStage); }
-  __device__ float* scores() const { return reinterpret_cast<float*>(base + F::kStage + F::kTableBytes); }
-  __device__ float* sums() const { return scores() + 128 * G; }
-  __device__ uint64_t* bar(int s) const { return reinterpret_cast<uint64_t*>(base + F::kFixed) + s; }
-};
-
-struct FlatCursor {
-  long bhc;        // (sequence * kv_heads + head) * chunks + chunk
-  int i;           // item of the (row, chunk)
-  ItemList items;  // of the sequence
-};
-
-__device__ __forceinline__ ItemList row_list(const WindowArgs& a, const NoPlan&, int) {
-  return item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len);
-}
-__device__ __forceinline__ ItemList row_list(const WindowArgs& a, const WindowPlan& p, int b) {
-  return item_list(a.queries, a.window, a.sinks, p.blocks[b], p.tail[b]);
-}
-
-// rpc: (row, chunk)s of a sequence.
-__device__ __forceinline__ FlatCursor flat_at(const WindowArgs& a, const NoPlan& p, int, long x) {
-  FlatCursor c;
-  c.items = row_list(a, p, 0);
-  c.bhc = x / c.items.n;
-  c.i = (int)(x - c.bhc * c.items.n);
-  return c;
-}
-__device__ __forceinline__ FlatCursor flat_at(const WindowArgs& a, const WindowPlan& p, int rpc, long x) {
-  int lo = 0, hi = a.batch;  // the last sequence whose first item is <= x has items
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.base[mid] <= x) lo = mid; else hi = mid;
-  }
-  FlatCursor c;
-  c.items = row_list(a, p, lo);
-  const long r = x - p.base[lo];
-  c.bhc = (long)lo * rpc + r / c.items.n;
-  c.i = (int)(r % c.items.n);
-  return c;
-}
-template <class Plan>
-__device__ __forceinline__ void flat_next(const WindowArgs& a, const Plan& p, int rpc, FlatCursor& c) {
-  if (++c.i < c.items.n) return;
-  c.i = 0;
-  ++c.bhc;
-  if constexpr (std::is_same<Plan, WindowPlan>::value) {
-    if (c.bhc % rpc == 0) {  // the next sequence that has items
-      int b = (int)(c.bhc / rpc);
-      while (b < a.batch && p.base[b + 1] == p.base[b]) ++b;
-      if (b < a.batch) c.items = row_list(a, p, b);
-      c.bhc = (long)b * rpc;
-    }
-  }
-}
-
-// Where the index entry and the permutation of a row's logical block j are (-1: the block
-// table names no block).
-__device__ __forceinline__ long entry_of(const WindowArgs& a, int b, int h, int j) {
-  if (a.block_table == nullptr) return ((long)b * a.kv_heads + h) * a.max_blocks + j;
-  const int p = a.block_table[(size_t)b * a.max_blocks + j];
-  if (p < 0 || (long)p >= (long)a.batch * a.max_blocks) return -1;
-  return ((long)(p / a.max_blocks) * a.kv_heads + h) * a.max_blocks + p % a.max_blocks;
-}
-
-// {kind, checked} of an index entry.
-template <int BITS>
-__device__ __forceinline__ int entry_kind(const WindowArgs& a, uint2 e) {
-  constexpr uint32_t raw = (uint32_t)raw_record_bytes(BITS);
-  const bool valid = e.x != 0xFFFFFFFFu && e.y >= 1040 / 16 && e.y * 16u <= raw && (uint64_t)e.x + e.y <= a.arena16;
-  return !valid ? kKindInvalid : (e.y * 16u == raw ? kKindRaw : kKindPacked);
-}
-
-// What a query row sees of the 128 (or fewer) tokens from pos0 on, as bounds on the offset
-// r from pos0: lo < r <= hi, or r < first.
-struct Seen {
-  int lo, hi, first;
-  __device__ bool all() const { return hi >= 127 && (lo < 0 || first > 127); }
-  __device__ bool operator()(int r) const { return r <= hi && (r > lo || r < first); }
-};
-__device__ __forceinline__ int clamp_offset(long long x) { return (int)(x < -1 ? -1 : (x > 128 ? 128 : x)); }
-__device__ __forceinline__ Seen seen_of(long long p, long long pos0, int window, int sinks) {
-  return {clamp_offset(p - window - pos0), clamp_offset(p - pos0), clamp_offset(sinks - pos0)};
+  __syncwarp();
 }
 
 // Scores of n <= 32 tail tokens on the CUDA cores: lane = token.
 template <int G>
-__device__ __forceinline__ void flat_tail_scores(const uint16_t* tail, const uint16_t* q, int n, float scale, float* sc,
+__device__ __forceinline__ void tail_scores_lanes(const uint16_t* tail, const uint16_t* q, int n, float scale, float* sc,
                                                  int lane) {
   float s[G];
 #pragma unroll
@@ -681,7 +384,7 @@ __device__ __forceinline__ void flat_tail_scores(const uint16_t* tail, const uin
 // Adds sum_t p[head][t] v[t][c]: lane = channels 4*lane + i.  Tokens of zero weight (masked
 // ones) are left out, so an infinity or NaN there does not spread.
 template <int G>
-__device__ __forceinline__ void flat_tail_values(const uint16_t* tail, const float* sc, int n, float* sacc, int lane) {
+__device__ __forceinline__ void tail_values_lanes(const uint16_t* tail, const float* sc, int n, float* sacc, int lane) {
   float4 s[G];
 #pragma unroll
   for (int hd = 0; hd < G; ++hd) s[hd] = reinterpret_cast<const float4*>(sacc + hd * 128)[lane];
@@ -706,103 +409,120 @@ __device__ __forceinline__ void flat_tail_values(const uint16_t* tail, const flo
   __syncwarp();
 }
 
-constexpr int kPartFloats = 132;  // per (slot, query row): 128 sums, maximum, sum of exp, pad
 
-// Warp sums of the (row, chunk) just done, to slot warp + bhc, and a fresh start.
-template <int G>
-__device__ __forceinline__ void flat_flush(const WindowArgs& a, long bhc, int warp, float* sacc,
-                                           float (&acc_lo)[I8Layout<G>::kNH][8], float (&acc_hi)[I8Layout<G>::kNH][8],
-                                           float (&mp)[G], float (&mrun)[G], float (&lrun)[G], int lane) {
-  using L = I8Layout<G>;
-  const int g = lane >> 2, t = lane & 3;
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < L::kNH; ++j) {
-    float* row = sacc + L::head(j, t) * 128 + g;
-#pragma unroll
-    for (int T8 = 0; T8 < 8; ++T8) {
-      if (L::owns(j, t)) {
-        row[16 * T8] += acc_lo[j][T8];
-        row[16 * T8 + 8] += acc_hi[j][T8];
-      }
-      acc_lo[j][T8] = acc_hi[j][T8] = 0.f;
-    }
+// ---- the kernel --------------------------------------------------------------------
+// A warp takes an item at a time.  Two ways to share the items out:
+//  * even split (kEven): the items of all (row, chunk)s in one list, an equal contiguous
+//    part for every warp the device holds.  A warp stages an item's K record, then its V
+//    record in the same stage (half the shared memory, so more warps per SM), and at each
+//    (row, chunk) border writes its sums to the workspace; window_merge_kernel joins them.
+//  * a cluster per (row, chunk): its warps take the items in turn, K and V records in
+//    flight together, and the sums are joined through (distributed) shared memory: one
+//    launch, for calls with few items.
+// Both join in a fixed order, so results do not depend on timing.
+template <int BITS, int G, bool kEven>
+struct WinCfg {
+  using C = Cfg<BITS, G, false>;
+  static constexpr int kStage = C::kStageRec;
+  static constexpr int kStages = kEven ? 1 : 2;
+  static constexpr int kTableBytes = (C::kI8Tab + 15) / 16 * 16;
+  static constexpr int kFixed = kStages * kStage + kTableBytes + 1024 * G;
+  static constexpr int kWarpSmem = (kFixed + 16 + 127) / 128 * 128;
+};
+
+// Warp-private shared memory: [K stage][V stage][table][scores][sums][2 mbarriers].
+template <int BITS, int G, bool kEven>
+struct WinMem {
+  using W = WinCfg<BITS, G, kEven>;
+  unsigned char* base;
+  __device__ unsigned char* stage(int v) const { return base + (kEven ? 0 : v) * W::kStage; }
+  __device__ uint32_t* table() const { return reinterpret_cast<uint32_t*>(base + W::kStages * W::kStage); }
+  __device__ float* scores() const {
+    return reinterpret_cast<float*>(base + W::kStages * W::kStage + W::kTableBytes);
   }
-  __syncwarp();
-  float* part = a.partials + (size_t)(warp + bhc) * G * kPartFloats;
-#pragma unroll
-  for (int hd = 0; hd < G; ++hd) {
-    const float mn = warp_sum(mp[hd]), l = warp_sum(lrun[hd]);
-    float4 s = reinterpret_cast<const float4*>(sacc + hd * 128)[lane];
-    s.x += mn;
-    s.y += mn;
-    s.z += mn;
-    s.w += mn;
-    __stcg(reinterpret_cast<float4*>(part + hd * kPartFloats) + lane, s);
-    if (lane == 0) __stcg(reinterpret_cast<float2*>(part + hd * kPartFloats + 128), make_float2(mrun[hd], l));
-    mp[hd] = 0.f;
-    mrun[hd] = kMinusInf;
-    lrun[hd] = 0.f;
-  }
-  __syncwarp();
-  zero_sums<G>(sacc, lane);
-  __syncwarp();
-}
+  __device__ float* sums() const { return scores() + 128 * G; }
+  __device__ uint64_t* bar(int v) const { return reinterpret_cast<uint64_t*>(base + W::kFixed) + v; }
+};
 
 // Resident CTAs per SM the register budget is sized for.
-constexpr int flat_min_ctas(int g) { return g == 1 ? 5 : 0; }
+constexpr int win_ctas(int g, bool even) { return even && g == 1 ? 5 : (even && g == 2 ? 4 : 0); }
 
-template <int BITS, int G, class Plan>
-__global__ void __launch_bounds__(kWinWarps * 32, flat_min_ctas(G))
-    window_flat_kernel(const WindowArgs a, const __grid_constant__ Plan plan) {
-  using F = FlatCfg<BITS, G>;
+template <int BITS, int G, bool kEven, class Plan>
+__global__ void __launch_bounds__(kWinWarps * 32, win_ctas(G, kEven))
+    window_kernel(const WindowArgs a, const __grid_constant__ Plan plan) {
+  using W = WinCfg<BITS, G, kEven>;
   using L = I8Layout<G>;
   constexpr int NH = L::kNH;
   extern __shared__ __align__(128) unsigned char smem[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int warp = blockIdx.x * kWinWarps + (threadIdx.x >> 5);
-  if (warp >= a.n_warps) return;
-  const FlatMem<BITS, G> m{smem + (threadIdx.x >> 5) * F::kWarpSmem};
-  const long lo = (long)((long long)a.n_items * warp / a.n_warps);
-  const long hi = (long)((long long)a.n_items * (warp + 1) / a.n_warps);
-  const int chunks = a.rows / G, rpc = a.kv_heads * chunks;
+  __shared__ float wmax[kWinWarps][G], wsum[kWinWarps][G], cmax[G], csum[G];  // cluster form
+  if constexpr (kEven) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunks = a.rows / G;
+  const WinMem<BITS, G, kEven> m{smem + warp * W::kWarpSmem};
+
+  // this warp's items
+  ItemCursor cc;
+  int n_mine, step = 1, ranks = 1, rank = 0;
+  const int part = blockIdx.x * kWinWarps + warp;  // of the even split
+  if constexpr (kEven) {
+    if (part >= a.n_parts) return;
+    const long lo = (long)((long long)a.n_items * part / a.n_parts);
+    n_mine = (int)((long)((long long)a.n_items * (part + 1) / a.n_parts) - lo);
+    cc = item_at(a, plan, chunks, lo);
+  } else {
+    cg::cluster_group cluster = cg::this_cluster();
+    ranks = (int)cluster.num_blocks();
+    rank = (int)cluster.block_rank();
+    step = ranks * kWinWarps;
+    const int rc = blockIdx.x / ranks, r = rc / chunks;
+    cc.chunk = rc - r * chunks;
+    cc.b = r / a.kv_heads;
+    cc.h = r - cc.b * a.kv_heads;
+    cc.items = row_list(a, plan, cc.b);
+    cc.i = warp * ranks + rank;  // neighbours in the list on different SMs
+    n_mine = cc.i < cc.items.n ? (cc.items.n - cc.i + step - 1) / step : 0;
+  }
+  auto next = [&](ItemCursor& c) {
+    if constexpr (kEven) item_next(a, plan, chunks, c);
+    else c.i += step;
+  };
+  // lanes 0 and 1 load an item's K and V entry
+  auto load_entry = [&](const ItemCursor& c) {
+    uint2 e = make_uint2(0u, 0u);
+    const int j = c.block();
+    if (lane < 2 && j < c.items.nb) {
+      const long at = entry_of(a, c.b, c.h, j);
+      e = at < 0 ? make_uint2(0xFFFFFFFFu, 0u)
+                 : *reinterpret_cast<const uint2*>((lane == 0 ? a.k_index : a.v_index) + at * 2);
+    }
+    return e;
+  };
+  // lane v issues its record (K: 0, V: 1)
+  auto issue = [&](int v, bool tail, uint2 e) {
+    if (lane == v) {
+      const int kind = tail ? kKindTail : entry_kind<BITS>(a, e);
+      fence_async_smem();
+      if (kind == kKindRaw || kind == kKindPacked) {
+        mbar_arrive_expect_tx(m.bar(v), e.y * 16u);
+        bulk_g2s(m.stage(v), (v ? a.v_arena : a.k_arena) + (uint64_t)e.x * 16, e.y * 16u, m.bar(v));
+      } else {
+        mbar_arrive(m.bar(v));
+      }
+    }
+    __syncwarp();
+  };
+  uint2 ent = make_uint2(0u, 0u);
+  if (n_mine > 0) ent = load_entry(cc);
   if (lane == 0) {
     mbar_init(m.bar(0), 1);
     mbar_init(m.bar(1), 1);
     fence_mbar_init();
   }
   __syncwarp();
-  // lane 0 and 1 load the K and V entry of an item ({0, 0} for a piece of the tail)
-  auto load_entry = [&](const FlatCursor& c) {
-    const int j = c.i < c.items.front ? c.i : c.items.from + (c.i - c.items.front);
-    uint2 e = make_uint2(0u, 0u);
-    if (lane < 2 && j < c.items.nb) {
-      const int bh = (int)(c.bhc / chunks), b = bh / a.kv_heads;
-      const long at = entry_of(a, b, bh - b * a.kv_heads, j);
-      e = at < 0 ? make_uint2(0xFFFFFFFFu, 0u)
-                 : *reinterpret_cast<const uint2*>((lane == 0 ? a.k_index : a.v_index) + at * 2);
-    }
-    return e;
-  };
-  // lane s issues its record (K: s = 0, V: s = 1)
-  auto issue = [&](int s, bool tail, uint2 e) {
-    if (lane == s) {
-      const int kind = tail ? kKindTail : entry_kind<BITS>(a, e);
-      fence_async_smem();
-      if (kind == kKindRaw || kind == kKindPacked) {
-        mbar_arrive_expect_tx(m.bar(s), e.y * 16u);
-        bulk_g2s(m.stage(), (s ? a.v_arena : a.k_arena) + (uint64_t)e.x * 16, e.y * 16u, m.bar(s));
-      } else {
-        mbar_arrive(m.bar(s));
-      }
-    }
-    __syncwarp();
-  };
-  FlatCursor cc = flat_at(a, plan, rpc, lo);
-  uint2 ent = load_entry(cc);
-  auto is_tail = [](const FlatCursor& c) { return c.i >= c.items.front + (c.items.nb - c.items.from); };
-  issue(0, is_tail(cc), ent);
+  if (n_mine > 0) {
+    issue(0, cc.block() >= cc.items.nb, ent);
+    if (!kEven) issue(1, cc.block() >= cc.items.nb, ent);
+  }
 
   float qr[G][4], mrun[G], lrun[G], mp[G];
   float acc_lo[NH][8], acc_hi[NH][8];
@@ -820,17 +540,49 @@ __global__ void __launch_bounds__(kWinWarps * 32, flat_min_ctas(G))
   float* sc = m.scores();
   zero_sums<G>(sacc, lane);
   __syncwarp();
-  long cur = -1;
+  const int g = lane >> 2, t = lane & 3;
+  // the tensor-core accumulators and min terms into the channel sums; l over the warp
+  auto collect = [&]() {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NH; ++j) {
+      float* row = sacc + L::head(j, t) * 128 + g;
+#pragma unroll
+      for (int T8 = 0; T8 < 8; ++T8) {
+        if (L::owns(j, t)) {
+          row[16 * T8] += acc_lo[j][T8];
+          row[16 * T8 + 8] += acc_hi[j][T8];
+        }
+        acc_lo[j][T8] = acc_hi[j][T8] = 0.f;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int hd = 0; hd < G; ++hd) {
+      const float mn = warp_sum(mp[hd]);
+      lrun[hd] = warp_sum(lrun[hd]);
+      float4* row = reinterpret_cast<float4*>(sacc + hd * 128) + lane;
+      float4 s = *row;
+      s.x += mn;
+      s.y += mn;
+      s.z += mn;
+      s.w += mn;
+      *row = s;
+      mp[hd] = 0.f;
+    }
+  };
+  bool fresh = true;  // the next item begins a (row, chunk)
+  long slot = 0;      // of the current one
+  const uint16_t* qrow = nullptr;
+  WholeBlocks whole_of{0, -1, -1};
   uint32_t phase = 0u;
-  const int t = lane & 3;
 #pragma unroll 1
-  for (long x = lo; x < hi; ++x, phase ^= 1u) {
-    const int bh = (int)(cc.bhc / chunks), chunk = (int)(cc.bhc - (long)bh * chunks);
-    const int b = bh / a.kv_heads, h = bh - b * a.kv_heads;
-    const uint16_t* qrow = a.q + ((size_t)bh * a.rows + (size_t)chunk * G) * 128;
-    if (cc.bhc != cur) {
-      if (cur >= 0) flat_flush<G>(a, cur, warp, sacc, acc_lo, acc_hi, mp, mrun, lrun, lane);
-      cur = cc.bhc;
+  for (int x = 0; x < n_mine; ++x, phase ^= 1u) {
+    if (fresh) {
+      fresh = false;
+      slot = cc.row(a, chunks);
+      qrow = a.q + (size_t)slot * G * 128;
+      whole_of = whole_blocks(a, cc.items);
 #pragma unroll
       for (int hd = 0; hd < G; ++hd) {
         const uint2 v = *reinterpret_cast<const uint2*>(qrow + hd * 128 + 4 * lane);
@@ -842,61 +594,64 @@ __global__ void __launch_bounds__(kWinWarps * 32, flat_min_ctas(G))
         qr[hd][3] = w.y;
       }
     }
-    const bool tail = is_tail(cc);
-    const int j = cc.i < cc.items.front ? cc.i : cc.items.from + (cc.i - cc.items.front);
+    const int j = cc.block();
+    const bool tail = j >= cc.items.nb;
     const int piece = tail ? j - cc.items.nb : 0;
     const int n_tok = tail ? min(kTailPiece, cc.items.tl - piece * kTailPiece) : 128;
-    const size_t tail_at = ((size_t)bh * 128 + piece * kTailPiece) * 128;
-    const long long pos0 = tail ? (long long)cc.items.nb * 128 + piece * kTailPiece : (long long)j * 128;
-    const long long p0 = (long long)cc.items.nb * 128 + cc.items.tl - a.queries;
-    const bool whole = !tail && seen_of(p0, pos0, a.window, a.sinks).hi >= 127 &&
-                       seen_of(p0 + a.queries - 1, pos0, a.window, a.sinks).all();
+    const size_t tail_at = (((size_t)cc.b * a.kv_heads + cc.h) * 128 + piece * kTailPiece) * 128;
+    const bool whole = !tail && whole_of(j);
     uint32_t slots = 0x03020100u + 0x04040404u * (uint32_t)lane;  // this lane's four slots' tokens
     if (!tail && !whole && a.perm != nullptr) {
-      const long at = entry_of(a, b, h, j);
-      if (at >= 0) slots = reinterpret_cast<const uint32_t*>(a.perm + at * 128)[lane];
+      const long at = entry_of(a, cc.b, cc.h, j);
+      if (at >= 0)  // asked for now, needed behind the scores
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(slots) : "l"(a.perm + at * 128 + 4 * lane));
     }
-    FlatCursor nc = cc;
-    flat_next(a, plan, rpc, nc);
-    const uint2 ent_next = x + 1 < hi ? load_entry(nc) : make_uint2(0u, 0u);
+    ItemCursor nc = cc;
+    next(nc);
+    const uint2 ent_next = x + 1 < n_mine ? load_entry(nc) : make_uint2(0u, 0u);
+    const bool tail_next = nc.block() >= nc.items.nb;
     const int len_k = (int)__shfl_sync(0xffffffffu, ent.y, 0), len_v = (int)__shfl_sync(0xffffffffu, ent.y, 1);
     const int kind_of_lane = entry_kind<BITS>(a, ent);
     const int kind_k = __shfl_sync(0xffffffffu, kind_of_lane, 0), kind_v = __shfl_sync(0xffffffffu, kind_of_lane, 1);
 
     // ---- scores ----
-    if (!mbar_wait_bounded(m.bar(0), phase, a.ctrl)) return;  // never landed (status set); nothing else in flight
+    if (!mbar_wait_bounded(m.bar(0), phase, a.ctrl)) {  // never landed (status set)
+      if (!kEven) mbar_wait_bounded(m.bar(1), phase, a.ctrl);
+      break;
+    }
     bool ok = true;
-    if (tail)
-      flat_tail_scores<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
-    else if (kind_k == kKindInvalid)
+    if (tail) {
+      if constexpr (kEven && G <= 2) tail_scores_lanes<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
+      else tail_scores32<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
+    } else if (kind_k == kKindInvalid) {
       ok = false;
-    else
-      ok = record_scores<BITS, G>(m.stage(), kind_k | (len_k << 8), m.table(), qr, sc, a.scale, lane);
+    } else {
+      ok = record_scores<BITS, G>(m.stage(0), kind_k | (len_k << 8), m.table(), qr, sc, a.scale, lane);
+    }
     __syncwarp();
-    issue(1, tail, ent);
+    if (kEven) issue(1, tail, ent);
+    else if (x + 1 < n_mine) issue(0, tail_next, ent_next);
 
     // ---- masks and the running softmax ----
     float pr[G][4];
 #pragma unroll
     for (int hd = 0; hd < G; ++hd) {
-      float sv[4];
-      float bm = kMinusInf;
       const float4 s4 = *reinterpret_cast<const float4*>(sc + hd * 128 + 4 * lane);
-      const float ss[4] = {s4.x, s4.y, s4.z, s4.w};
-      if (whole) {
+      float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+      if (!ok) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sv[i] = ok ? ss[i] : kMinusInf;
-      } else {
-        const Seen see = seen_of(p0 + (chunk * G + hd) / a.group, pos0, a.window, a.sinks);
+        for (int i = 0; i < 4; ++i) sv[i] = kMinusInf;
+      } else if (!whole) {
+        const long long pos0 = tail ? (long long)cc.items.nb * 128 + piece * kTailPiece : (long long)j * 128;
+        const long long p0 = (long long)cc.items.nb * 128 + cc.items.tl - a.queries;
+        const Seen see = seen_of(p0 + (cc.chunk * G + hd) / a.group, pos0, a.window, a.sinks);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = (int)((slots >> (8 * i)) & 0xFFu);
-          sv[i] = ok && see(r) && (!tail || r < n_tok) ? ss[i] : kMinusInf;
+          if (!see(r) || r >= n_tok) sv[i] = kMinusInf;
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bm = fmaxf(bm, sv[i]);
-      bm = warp_max(bm);
+      const float bm = warp_max(fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3])));
       const float m_new = fmaxf(mrun[hd], bm);
       float ps = 0.f;
 #pragma unroll
@@ -905,10 +660,10 @@ __global__ void __launch_bounds__(kWinWarps * 32, flat_min_ctas(G))
         ps += pr[hd][i];
       }
       if (m_new > mrun[hd]) {  // warp-uniform: rescale what was summed under the old maximum
-        const float alpha = mrun[hd] == kMinusInf ? 0.f : exp2f((mrun[hd] - m_new) * kWinLog2e);
-        lrun[hd] *= alpha;
-        mp[hd] *= alpha;
         if (mrun[hd] != kMinusInf) {
+          const float alpha = exp2f((mrun[hd] - m_new) * kWinLog2e);
+          lrun[hd] *= alpha;
+          mp[hd] *= alpha;
           float4* row = reinterpret_cast<float4*>(sacc + hd * 128) + lane;
           const float4 r4 = *row;
           *row = make_float4(r4.x * alpha, r4.y * alpha, r4.z * alpha, r4.w * alpha);
@@ -925,30 +680,113 @@ __global__ void __launch_bounds__(kWinWarps * 32, flat_min_ctas(G))
         }
         mrun[hd] = m_new;
       }
-      lrun[hd] += ps;  // of this lane's slots; summed over the warp at the flush
+      lrun[hd] += ps;  // of this lane's slots; summed over the warp by collect()
     }
 
     // ---- values ----
-    if (!mbar_wait_bounded(m.bar(1), phase, a.ctrl)) return;
+    if (!mbar_wait_bounded(m.bar(1), phase, a.ctrl)) {
+      if (!kEven && x + 1 < n_mine) mbar_wait_bounded(m.bar(0), phase ^ 1u, a.ctrl);
+      break;
+    }
     if (tail) {
       __syncwarp();
 #pragma unroll
       for (int hd = 0; hd < G; ++hd)
         *reinterpret_cast<float4*>(sc + hd * 128 + 4 * lane) = make_float4(pr[hd][0], pr[hd][1], pr[hd][2], pr[hd][3]);
       __syncwarp();
-      flat_tail_values<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
+      if constexpr (kEven && G <= 2) tail_values_lanes<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
+      else tail_values32<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
     } else if (kind_v == kKindInvalid) {
       ok = false;
     } else if (ok) {
-      ok = record_values<BITS, G>(m.stage(), kind_v | (len_v << 8), m.table(), pr, acc_lo, acc_hi, sacc, mp, lane);
+      ok = record_values<BITS, G>(m.stage(1), kind_v | (len_v << 8), m.table(), pr, acc_lo, acc_hi, sacc, mp, lane);
     }
     if (!ok && lane == 0) set_status(a.ctrl, PACKKV_DEV_BAD_RECORD);
     __syncwarp();
-    if (x + 1 < hi) issue(0, is_tail(nc), ent_next);
+    if (x + 1 < n_mine) issue(kEven ? 0 : 1, tail_next, ent_next);
     cc = nc;
     ent = ent_next;
+    if constexpr (kEven) {
+      fresh = cc.i == 0 || x + 1 == n_mine;
+      if (fresh) {  // the (row, chunk) is done here: its sums to slot part + row
+        collect();
+        float* out = a.partials + (size_t)(part + slot) * G * kPartFloats;
+#pragma unroll
+        for (int hd = 0; hd < G; ++hd) {
+          __stcg(reinterpret_cast<float4*>(out + hd * kPartFloats) + lane,
+                 reinterpret_cast<const float4*>(sacc + hd * 128)[lane]);
+          if (lane == 0)
+            __stcg(reinterpret_cast<float2*>(out + hd * kPartFloats + 128), make_float2(mrun[hd], lrun[hd]));
+          mrun[hd] = kMinusInf;
+          lrun[hd] = 0.f;
+        }
+        __syncwarp();
+        zero_sums<G>(sacc, lane);
+        __syncwarp();
+      }
+    }
   }
-  if (cur >= 0) flat_flush<G>(a, cur, warp, sacc, acc_lo, acc_hi, mp, mrun, lrun, lane);
+
+  if constexpr (!kEven) {
+    // this warp's sums, then the CTA's, then the cluster's
+    collect();
+#pragma unroll
+    for (int hd = 0; hd < G; ++hd) {
+      if (lane == 0) {
+        wmax[warp][hd] = mrun[hd];
+        wsum[warp][hd] = lrun[hd];
+      }
+    }
+    __syncthreads();
+    float* cta = WinMem<BITS, G, kEven>{smem}.scores();  // [G][128], free now
+    for (int o = threadIdx.x; o < G * 128; o += kWinWarps * 32) {
+      const int hd = o >> 7;
+      float M = wmax[0][hd];
+#pragma unroll
+      for (int w = 1; w < kWinWarps; ++w) M = fmaxf(M, wmax[w][hd]);
+      float s = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWinWarps; ++w) {
+        const float e = wsum[w][hd] == 0.f ? 0.f : exp2f((wmax[w][hd] - M) * kWinLog2e);
+        if (e != 0.f) s = fmaf(WinMem<BITS, G, kEven>{smem + w * W::kWarpSmem}.sums()[o], e, s);
+        l = fmaf(wsum[w][hd], e, l);
+      }
+      cta[o] = s;
+      if ((o & 127) == 0) {
+        cmax[hd] = M;
+        csum[hd] = l;
+      }
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    if (ranks > 1) cluster.sync(); else __syncthreads();
+    float* orow = a.out + (size_t)(blockIdx.x / ranks) * G * 128;
+    for (int o = rank * kWinWarps * 32 + threadIdx.x; o < G * 128; o += ranks * kWinWarps * 32) {
+      const int hd = o >> 7;
+      float mr[kMaxRanks], lr[kMaxRanks], y[kMaxRanks];  // all ranks' loads in flight
+#pragma unroll
+      for (int r = 0; r < kMaxRanks; ++r) {
+        mr[r] = kMinusInf;
+        lr[r] = y[r] = 0.f;
+        if (r < ranks) {
+          mr[r] = *cluster.map_shared_rank(&cmax[hd], r);
+          lr[r] = *cluster.map_shared_rank(&csum[hd], r);
+          y[r] = *cluster.map_shared_rank(&cta[o], r);
+        }
+      }
+      float M = mr[0];
+#pragma unroll
+      for (int r = 1; r < kMaxRanks; ++r) M = fmaxf(M, mr[r]);
+      float s = 0.f, l = 0.f;
+#pragma unroll
+      for (int r = 0; r < kMaxRanks; ++r) {
+        const float e = lr[r] == 0.f ? 0.f : exp2f((mr[r] - M) * kWinLog2e);
+        if (e != 0.f) s = fmaf(y[r], e, s);
+        l = fmaf(lr[r], e, l);
+      }
+      orow[o] = l == 0.f ? 0.f : s / l;  // a row that sees nothing is zero; a NaN stays one
+    }
+    if (ranks > 1) cluster.sync();  // no CTA leaves while another reads its sums
+  }
 }
 
 // Joins the slots of every output row with the log-sum-exp rule in a fixed order: one CTA
@@ -975,7 +813,7 @@ __global__ void __launch_bounds__(128) window_merge_kernel(const WindowArgs a, i
   else
     first = bhc * items.n;
   // warp whose range [w*N/W, (w+1)*N/W) holds an item
-  auto warp_of = [&](long item) { return (long)(((long long)(item + 1) * a.n_warps + a.n_items - 1) / a.n_items) - 1; };
+  auto warp_of = [&](long item) { return (long)(((long long)(item + 1) * a.n_parts + a.n_items - 1) / a.n_items) - 1; };
   const long w0 = warp_of(first), w1 = warp_of(first + items.n - 1);
   const float* base = a.partials + hd * kPartFloats;
   const size_t stride = (size_t)group * kPartFloats;
@@ -1031,119 +869,112 @@ struct WinKernel {
 };
 
 template <class Plan>
-bool win_select(int bits, int g, bool flat, WinKernel* k) {
+WinKernel win_select(int bits, int g, bool even) {
 #define PACKKV_WCASE(B, GG)                                                                                         \
-  if (bits == B && g == GG) {                                                                                       \
-    *k = flat ? WinKernel{reinterpret_cast<const void*>(&window_flat_kernel<B, GG, Plan>),                          \
-                          kWinWarps * FlatCfg<B, GG>::kWarpSmem}                                                    \
-              : WinKernel{reinterpret_cast<const void*>(&window_kernel<B, GG, Plan>), kWinWarps * WinCfg<B, GG>::kWarpSmem}; \
-    return true;                                                                                                    \
-  }
+  if (bits == B && g == GG)                                                                                         \
+    return even ? WinKernel{reinterpret_cast<const void*>(&window_kernel<B, GG, true, Plan>),                       \
+                            kWinWarps * WinCfg<B, GG, true>::kWarpSmem}                                             \
+                : WinKernel{reinterpret_cast<const void*>(&window_kernel<B, GG, false, Plan>),                      \
+                            kWinWarps * WinCfg<B, GG, false>::kWarpSmem};
   PACKKV_WCASE(4, 1) PACKKV_WCASE(4, 2) PACKKV_WCASE(4, 4) PACKKV_WCASE(4, 8)
   PACKKV_WCASE(3, 1) PACKKV_WCASE(3, 2) PACKKV_WCASE(3, 4) PACKKV_WCASE(3, 8)
   PACKKV_WCASE(2, 1) PACKKV_WCASE(2, 2) PACKKV_WCASE(2, 4) PACKKV_WCASE(2, 8)
 #undef PACKKV_WCASE
-  return false;
+  return {nullptr, 0};
 }
 
-struct Residency {
-  int sms, warps;  // warps of the kernel that the device holds
-};
-
-// Raises the kernel's shared memory limit once per device; SMs and resident warps.
-cudaError_t win_configure(const WinKernel& k, Residency* r) {
+// Raises the kernel's shared memory limit once per device; CTAs that the device holds.
+cudaError_t win_configure(const WinKernel& k, int* ctas) {
   static std::mutex mu;
-  static std::unordered_map<long long, Residency> done;
-  int dev = 0;
+  static std::unordered_map<long long, int> done;
+  int dev = 0, sms = 0, per_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const long long key = (long long)(reinterpret_cast<uintptr_t>(k.fn)) * 64 + dev;
   std::lock_guard<std::mutex> lock(mu);
   auto it = done.find(key);
   if (it != done.end()) {
-    *r = it->second;
+    *ctas = it->second;
     return cudaSuccess;
   }
   e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-  if (e != cudaSuccess) return e;
-  e = cudaDeviceGetAttribute(&r->sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, kWinWarps * 32, k.smem);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, kWinWarps * 32, (size_t)k.smem);
   if (e != cudaSuccess) return e;
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  r->warps = r->sms * per_sm * kWinWarps;
-  done[key] = *r;
+  done[key] = *ctas = sms * per_sm;
   return cudaSuccess;
 }
 
-int max_flat_warps() {
+// Warps that an even split may have (workspace slots): at most 32 per SM.
+int max_parts() {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   return sms * 32;
 }
 
 template <class Plan>
-cudaError_t launch_window_t(WindowArgs a, const Plan& plan, cudaStream_t stream) {
-  const int g = a.rows < 8 ? a.rows : 8;
+cudaError_t launch_window_t(WindowArgs a, const Plan& plan, int g, cudaStream_t stream) {
   const long row_chunks = (long)a.batch * a.kv_heads * (a.rows / g);
-  WinKernel k{};
-  Residency r{};
-  if (!win_select<Plan>(a.bits, g, true, &k)) return cudaErrorInvalidValue;
-  cudaError_t e = win_configure(k, &r);
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  void* args[] = {&a, const_cast<Plan*>(&plan)};
+  WinKernel k = win_select<Plan>(a.bits, g, true);
+  int ctas = 0;
+  cudaError_t e = win_configure(k, &ctas);
   if (e != cudaSuccess) return e;
-  if (a.n_items >= r.warps) {
-    a.n_warps = r.warps < max_flat_warps() ? r.warps : max_flat_warps();
-    void* args[] = {&a, const_cast<Plan*>(&plan)};
-    e = cudaLaunchKernel(k.fn, dim3((unsigned)((a.n_warps + kWinWarps - 1) / kWinWarps)), dim3(kWinWarps * 32), args,
+  if (a.n_items >= (long)ctas * kWinWarps) {
+    a.n_parts = ctas * kWinWarps < max_parts() ? ctas * kWinWarps : max_parts();
+    e = cudaLaunchKernel(k.fn, dim3((unsigned)((a.n_parts + kWinWarps - 1) / kWinWarps)), dim3(kWinWarps * 32), args,
                          (size_t)k.smem, stream);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(row_chunks * g));
     cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, &window_merge_kernel<Plan>, a, g, plan);
   }
-  if (!win_select<Plan>(a.bits, g, false, &k)) return cudaErrorInvalidValue;
-  e = win_configure(k, &r);
+  k = win_select<Plan>(a.bits, g, false);
+  e = win_configure(k, &ctas);
   if (e != cudaSuccess) return e;
   int ranks = 1;
-  while (ranks < 8 && ranks * kWinWarps < a.most_items && row_chunks * ranks * 2 <= 2L * r.sms) ranks *= 2;
-  cudaLaunchConfig_t cfg{};
+  while (ranks < kMaxRanks && ranks * kWinWarps < a.most_items && row_chunks * ranks * 2 <= ctas) ranks *= 2;
   cfg.gridDim = dim3((unsigned)(row_chunks * ranks));
   cfg.blockDim = dim3(kWinWarps * 32);
   cfg.dynamicSmemBytes = (size_t)k.smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void* args[] = {&a, const_cast<Plan*>(&plan)};
   return cudaLaunchKernelExC(&cfg, k.fn, args);
+}
+
+// Query rows of a chunk.
+int chunk_rows(const WindowArgs& a) {
+  const char* env = getenv("PACKKV_WIN_G");
+  int g = a.rows < 8 ? a.rows : 8;
+  if (env && atoi(env) < g) g = atoi(env);
+  return g;
 }
 
 }  // namespace
 
 size_t window_workspace_bytes(int batch, int kv_heads, int rows) {
-  const int g = rows < 8 ? rows : 8;
-  return ((size_t)max_flat_warps() + (size_t)batch * kv_heads * (rows / g)) * g * kPartFloats * sizeof(float);
+  // slots are (parts + rows * chunks) * chunk rows: at most this for any chunk size
+  return ((size_t)max_parts() * (rows < 8 ? rows : 8) + (size_t)batch * kv_heads * rows) * kPartFloats * sizeof(float);
 }
 
 cudaError_t launch_window(WindowArgs a, WindowPlan* plan, cudaStream_t stream) {
-  const int g = a.rows < 8 ? a.rows : 8;
+  const int g = chunk_rows(a);
   const long rpc = (long)a.kv_heads * (a.rows / g);
   if (plan == nullptr) {
-    a.most_items = a.row_items = item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len).n;
-    a.n_items = (long)a.batch * rpc * a.row_items;
-    return launch_window_t<NoPlan>(a, NoPlan{}, stream);
+    a.most_items = item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len).n;
+    a.n_items = (long)a.batch * rpc * a.most_items;
+    return launch_window_t<NoPlan>(a, NoPlan{}, g, stream);
   }
   a.n_items = 0;
   for (int b = 0; b < a.batch; ++b) {
@@ -1151,10 +982,10 @@ cudaError_t launch_window(WindowArgs a, WindowPlan* plan, cudaStream_t stream) {
     if (n > a.most_items) a.most_items = n;
     plan->base[b] = (int32_t)a.n_items;
     a.n_items += n * rpc;
+    if (a.n_items > 0x7fffffffL) return cudaErrorInvalidValue;
   }
-  if (a.n_items > 0x7fffffffL) return cudaErrorInvalidValue;
   plan->base[a.batch] = (int32_t)a.n_items;
-  return launch_window_t<WindowPlan>(a, *plan, stream);
+  return launch_window_t<WindowPlan>(a, *plan, g, stream);
 }
 
 }  // namespace packkv
