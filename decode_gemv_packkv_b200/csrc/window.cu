@@ -13,7 +13,6 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
-#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 #include <unordered_map>
@@ -445,7 +444,7 @@ struct WinMem {
 };
 
 // Resident CTAs per SM the register budget is sized for.
-constexpr int win_ctas(int g, bool even) { return even && g == 1 ? 5 : (even && g == 2 ? 4 : 0); }
+constexpr int win_ctas(int g, bool even) { return even ? (g == 1 ? 5 : (g == 2 ? 4 : 3)) : 0; }
 
 template <int BITS, int G, bool kEven, class Plan>
 __global__ void __launch_bounds__(kWinWarps * 32, win_ctas(G, kEven))
@@ -876,9 +875,9 @@ WinKernel win_select(int bits, int g, bool even) {
                             kWinWarps * WinCfg<B, GG, true>::kWarpSmem}                                             \
                 : WinKernel{reinterpret_cast<const void*>(&window_kernel<B, GG, false, Plan>),                      \
                             kWinWarps * WinCfg<B, GG, false>::kWarpSmem};
-  PACKKV_WCASE(4, 1) PACKKV_WCASE(4, 2) PACKKV_WCASE(4, 4) PACKKV_WCASE(4, 8)
-  PACKKV_WCASE(3, 1) PACKKV_WCASE(3, 2) PACKKV_WCASE(3, 4) PACKKV_WCASE(3, 8)
-  PACKKV_WCASE(2, 1) PACKKV_WCASE(2, 2) PACKKV_WCASE(2, 4) PACKKV_WCASE(2, 8)
+  PACKKV_WCASE(4, 1) PACKKV_WCASE(4, 2) PACKKV_WCASE(4, 4)
+  PACKKV_WCASE(3, 1) PACKKV_WCASE(3, 2) PACKKV_WCASE(3, 4)
+  PACKKV_WCASE(2, 1) PACKKV_WCASE(2, 2) PACKKV_WCASE(2, 4)
 #undef PACKKV_WCASE
   return {nullptr, 0};
 }
@@ -915,77 +914,121 @@ int max_parts() {
 }
 
 template <class Plan>
-cudaError_t launch_window_t(WindowArgs a, const Plan& plan, int g, cudaStream_t stream) {
-  const long row_chunks = (long)a.batch * a.kv_heads * (a.rows / g);
+cudaError_t even_split(WindowArgs a, const Plan& plan, int g, const WinKernel& k, int warps, cudaStream_t stream) {
+  a.n_parts = warps < max_parts() ? warps : max_parts();
+  if (a.n_items < a.n_parts) a.n_parts = (int)a.n_items;
+  void* args[] = {&a, const_cast<Plan*>(&plan)};
+  cudaError_t e = cudaLaunchKernel(k.fn, dim3((unsigned)((a.n_parts + kWinWarps - 1) / kWinWarps)),
+                                   dim3(kWinWarps * 32), args, (size_t)k.smem, stream);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.stream = stream;
-  void* args[] = {&a, const_cast<Plan*>(&plan)};
-  WinKernel k = win_select<Plan>(a.bits, g, true);
-  int ctas = 0;
-  cudaError_t e = win_configure(k, &ctas);
-  if (e != cudaSuccess) return e;
-  if (a.n_items >= (long)ctas * kWinWarps) {
-    a.n_parts = ctas * kWinWarps < max_parts() ? ctas * kWinWarps : max_parts();
-    e = cudaLaunchKernel(k.fn, dim3((unsigned)((a.n_parts + kWinWarps - 1) / kWinWarps)), dim3(kWinWarps * 32), args,
-                         (size_t)k.smem, stream);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(row_chunks * g));
-    cfg.blockDim = dim3(128);
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    return cudaLaunchKernelEx(&cfg, &window_merge_kernel<Plan>, a, g, plan);
-  }
-  k = win_select<Plan>(a.bits, g, false);
-  e = win_configure(k, &ctas);
-  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)((long)a.batch * a.kv_heads * a.rows));
+  cfg.blockDim = dim3(128);
+  return cudaLaunchKernelEx(&cfg, &window_merge_kernel<Plan>, a, g, plan);
+}
+
+template <class Plan>
+cudaError_t clusters(WindowArgs a, const Plan& plan, int g, const WinKernel& k, int ctas, cudaStream_t stream) {
+  const long row_chunks = (long)a.batch * a.kv_heads * (a.rows / g);
   int ranks = 1;
   while (ranks < kMaxRanks && ranks * kWinWarps < a.most_items && row_chunks * ranks * 2 <= ctas) ranks *= 2;
-  cfg.gridDim = dim3((unsigned)(row_chunks * ranks));
-  cfg.blockDim = dim3(kWinWarps * 32);
-  cfg.dynamicSmemBytes = (size_t)k.smem;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ranks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3((unsigned)(row_chunks * ranks));
+  cfg.blockDim = dim3(kWinWarps * 32);
+  cfg.dynamicSmemBytes = (size_t)k.smem;
+  void* args[] = {&a, const_cast<Plan*>(&plan)};
   return cudaLaunchKernelExC(&cfg, k.fn, args);
 }
 
-// Query rows of a chunk.
-int chunk_rows(const WindowArgs& a) {
-  const char* env = getenv("PACKKV_WIN_G");
-  int g = a.rows < 8 ? a.rows : 8;
-  if (env && atoi(env) < g) g = atoi(env);
-  return g;
+// Query rows of a chunk (1, 2 or 4) and the form.  A record's codes are read and masked
+// once per chunk, so larger chunks do less work in all; smaller ones spread it over more
+// warps.  Measured (us, E the even split, C clusters, digits the chunk's rows; uncompressed
+// records, and in brackets compressed ones):
+//   8 kv heads x 4 rows, 5 blocks:        C1 6.9  C2 8.2  C4 10.3  E1 10.6
+//   2 kv heads x 8 rows, 36 blocks:       C1 10.1 C2 11.4 E1 12.9  E2 13.1 (30 32 25 24)
+//   8 kv heads x 8 rows, 36 blocks:       C2 12.6 C1 13.6 E2 14.6  E4 15.9 (36 46 28 28)
+//   32 kv heads x 2 rows, 18 blocks:      C2 8.6  C1 10.6 E2 11.5          (21 31 22)
+//   2 x 32 kv heads x 4 rows, 18 blocks:  E2 15.1 E4 15.5 C2 16.1  C4 16.8 (35 30 52 42)
+//   16 x 8 kv heads x 4 rows, 33 blocks:  E2 28.7 E4 29.7 C4 32.7  E1 40.6 (124 87 102 210)
+// so: single rows while they give every scheduler of the device at most one item, pairs
+// while they fill at most half of the warps it holds, both in clusters; else four rows.
+template <class Plan>
+cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
+  long per_head = 0;  // items of one kv head over all sequences
+  if constexpr (std::is_same<Plan, WindowPlan>::value) {
+    for (int b = 0; b < a.batch; ++b) {
+      const int n = item_list(a.queries, a.window, a.sinks, plan.blocks[b], plan.tail[b]).n;
+      if (n > a.most_items) a.most_items = n;
+      per_head += n;
+    }
+  } else {
+    a.most_items = item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len).n;
+    per_head = (long)a.batch * a.most_items;
+  }
+  auto items = [&](int g) { return per_head * a.kv_heads * (a.rows / g); };
+  int sms = 0, dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  int g = a.rows < 4 ? a.rows : 4, ctas = 0;
+  bool cluster = false;
+  if (items(1) <= 4L * sms) {
+    g = 1;
+    cluster = true;
+  } else if (a.rows >= 2) {
+    e = win_configure(win_select<Plan>(a.bits, 2, true), &ctas);
+    if (e != cudaSuccess) return e;
+    if (2 * items(2) <= (long)ctas * kWinWarps) {
+      g = 2;
+      cluster = true;
+    }
+  }
+  const WinKernel even = win_select<Plan>(a.bits, g, true);
+  e = win_configure(even, &ctas);
+  if (e != cudaSuccess) return e;
+  cluster = cluster || 2 * items(g) <= (long)ctas * kWinWarps;
+  a.n_items = items(g);
+  if (a.n_items > 0x7fffffffL) return cudaErrorInvalidValue;
+  if constexpr (std::is_same<Plan, WindowPlan>::value) {
+    long at = 0;
+    for (int b = 0; b < a.batch; ++b) {
+      plan.base[b] = (int32_t)at;
+      at += (long)item_list(a.queries, a.window, a.sinks, plan.blocks[b], plan.tail[b]).n * a.kv_heads * (a.rows / g);
+    }
+    plan.base[a.batch] = (int32_t)at;
+  }
+  if (!cluster) return even_split(a, plan, g, even, ctas * kWinWarps, stream);
+  const WinKernel k = win_select<Plan>(a.bits, g, false);
+  e = win_configure(k, &ctas);
+  if (e != cudaSuccess) return e;
+  return clusters(a, plan, g, k, ctas, stream);
 }
 
 }  // namespace
 
 size_t window_workspace_bytes(int batch, int kv_heads, int rows) {
-  // slots are (parts + rows * chunks) * chunk rows: at most this for any chunk size
-  return ((size_t)max_parts() * (rows < 8 ? rows : 8) + (size_t)batch * kv_heads * rows) * kPartFloats * sizeof(float);
+  // (parts + (row, chunk)s) slots of a chunk's rows: at most this for any chunk
+  return ((size_t)max_parts() * (rows < 4 ? rows : 4) + (size_t)batch * kv_heads * rows) * kPartFloats * sizeof(float);
 }
 
 cudaError_t launch_window(WindowArgs a, WindowPlan* plan, cudaStream_t stream) {
-  const int g = chunk_rows(a);
-  const long rpc = (long)a.kv_heads * (a.rows / g);
-  if (plan == nullptr) {
-    a.most_items = item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len).n;
-    a.n_items = (long)a.batch * rpc * a.most_items;
-    return launch_window_t<NoPlan>(a, NoPlan{}, g, stream);
-  }
-  a.n_items = 0;
-  for (int b = 0; b < a.batch; ++b) {
-    const int n = item_list(a.queries, a.window, a.sinks, plan->blocks[b], plan->tail[b]).n;
-    if (n > a.most_items) a.most_items = n;
-    plan->base[b] = (int32_t)a.n_items;
-    a.n_items += n * rpc;
-    if (a.n_items > 0x7fffffffL) return cudaErrorInvalidValue;
-  }
-  plan->base[a.batch] = (int32_t)a.n_items;
-  return launch_window_t<WindowPlan>(a, *plan, g, stream);
+  if (plan != nullptr) return launch_window_p<WindowPlan>(a, *plan, stream);
+  NoPlan none;
+  return launch_window_p<NoPlan>(a, none, stream);
 }
 
 }  // namespace packkv
