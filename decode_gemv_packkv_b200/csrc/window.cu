@@ -443,11 +443,13 @@ struct WinMem {
   __device__ uint64_t* bar(int v) const { return reinterpret_cast<uint64_t*>(base + W::kFixed) + v; }
 };
 
-// Resident CTAs per SM the register budget is sized for.
-constexpr int win_ctas(int g, bool even) { return even ? (g == 1 ? 5 : (g == 2 ? 4 : 3)) : 0; }
+// Resident CTAs per SM the register budget of the even split is sized for.  Single rows, 16 x
+// 32 heads over 4096 tokens: four CTAs 61.1 / 64.3 / 47.4 us (4 / 3 / 2 bits), five (96
+// registers, a few of them spilled for 3 bits) 63.1 / 65.7 / 45.8, six 69 for 3 bits.
+constexpr int win_ctas(int bits, int g, bool even) { return !even ? 0 : (g == 1 ? (bits == 2 ? 5 : 4) : (g == 2 ? 4 : 3)); }
 
 template <int BITS, int G, bool kEven, class Plan>
-__global__ void __launch_bounds__(kWinWarps * 32, win_ctas(G, kEven))
+__global__ void __launch_bounds__(kWinWarps * 32, win_ctas(BITS, G, kEven))
     window_kernel(const WindowArgs a, const __grid_constant__ Plan plan) {
   using W = WinCfg<BITS, G, kEven>;
   using L = I8Layout<G>;

@@ -227,21 +227,21 @@ class PackKVCache:
         that were rejected, a sequence that is done) and caches filled from saved buffers;
         no device memory changes, so a longer length must already be there."""
         s = self.s
-        if not self.ragged:
-            old = s.n_blocks, s.tail_len
-            s.n_blocks, s.tail_len = blocks, tail
-        else:
-            if len(blocks) != s.batch or len(tail) != s.batch:
-                raise ValueError("set_lengths needs the blocks and the tail of every sequence")
-            old = self._seq_blocks[:], self._seq_tail[:]
+        if self.ragged and (len(blocks) != s.batch or len(tail) != s.batch):
+            raise ValueError("set_lengths needs the blocks and the tail of every sequence")
+        old = (self._seq_blocks[:], self._seq_tail[:]) if self.ragged else (s.n_blocks, s.tail_len)
+        try:
+            self._put_lengths(blocks, tail)
+            _check("packkv_cache_check", _lib.packkv_cache_check(ctypes.byref(s)))
+        except Exception:
+            self._put_lengths(*old)
+            raise
+
+    def _put_lengths(self, blocks, tail):
+        if self.ragged:
             self._seq_blocks[:], self._seq_tail[:] = blocks, tail
-        status = _lib.packkv_cache_check(ctypes.byref(s))
-        if status != OK:
-            if self.ragged:
-                self._seq_blocks[:], self._seq_tail[:] = old
-            else:
-                s.n_blocks, s.tail_len = old
-            _check("packkv_cache_check", status)
+        else:
+            self.s.n_blocks, self.s.tail_len = blocks, tail
 
     @property
     def bits(self) -> int:

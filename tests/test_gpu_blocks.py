@@ -276,3 +276,54 @@ def test_reset_sequence_and_reuse(pk):
     for _ in range(128):
         pk.packkv_append_token_masked(dst, k, k, [True, False])
     assert dst.seq_blocks == [1, 2] and pk.packkv_get_status(dst) == 0
+
+
+def test_captured_and_replayed(pk):
+    """Fork, free and compact in one graph, replayed after the source has changed."""
+    src = _filled(pk, 3, 2, 4, 4, [400, 256, 30], 21)
+    dst = pk.PackKVCache(3, 2, 4, 4, ragged=True, keep_perm=True)
+    lengths = src.seq_blocks, src.seq_tail
+    keep = src.k_index.clone(), src.v_index.clone()
+
+    def calls():
+        pk.packkv_fork_sequences(src, [0], [2])
+        pk.packkv_free_blocks(src, [0, 1, 0], [1, 1, 0])
+        pk.packkv_compact(dst, src)
+
+    calls()
+    torch.cuda.synchronize()
+    want = _snapshot(dst), dst.k_arena.clone()
+    src.set_lengths(*lengths)
+    src.k_index.copy_(keep[0])
+    src.v_index.copy_(keep[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for x in (dst.k_index, dst.v_index, dst.k_arena, dst.ctrl, dst.perm):
+        x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    n = dst.arena_used()[0]
+    for name, x in want[0].items():
+        assert torch.equal(getattr(dst, name), x), name
+    assert torch.equal(dst.k_arena[:n], want[1][:n])
+    _check_compacted(pk, dst, src)
+
+
+def test_lengths_are_checked(pk):
+    cache = pk.PackKVCache(2, 1, 3, 4, ragged=True)
+    cache.set_lengths([1, 3], [127, 0])
+    for bad in (([4, 0], [0, 0]), ([0, 0], [128, 0]), ([-1, 0], [0, 0])):
+        with pytest.raises(pk.PackKVError):
+            cache.set_lengths(*bad)
+    for bad in (([1], [0]), ([1, 1], [0])):
+        with pytest.raises(ValueError):
+            cache.set_lengths(*bad)
+    with pytest.raises(TypeError):
+        cache.set_lengths([0, 0], ["a", 0])
+    assert cache.seq_blocks == [1, 3] and cache.seq_tail == [127, 0]
+    flat = pk.PackKVCache(1, 1, 3, 4)
+    flat.set_lengths(2, 5)
+    with pytest.raises(pk.PackKVError):
+        flat.set_lengths(4)
+    assert (flat.n_blocks, flat.tail_len) == (2, 5)

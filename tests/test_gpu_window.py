@@ -205,9 +205,56 @@ def test_repeatable_and_in_a_graph(pk):
     assert torch.equal(out, want)
 
 
-def test_many_rows(pk):
-    """More rows than the device holds at once, and a long row on its own."""
-    cache, oc = _caches(pk, 20, 16, 2, [260 + 3 * b for b in range(20)], 15)
-    _check(pk, cache, oc, 1, 1, 200, 4, 1)
-    cache, oc = _caches(pk, 1, 1, 3, [128 * 70 + 77], 16)
-    _check(pk, cache, oc, 2, 1, 8500, 4, 2)
+@pytest.mark.parametrize("rows,queries", [(1, 1), (2, 2), (4, 1), (8, 4)])
+def test_many_sequences(pk, rows, queries):
+    """More items than half the device's warps (the even split): 64 sequences forked from two,
+    every one with queries of its own."""
+    B, H = 64, 8
+    k, v, _ = synth.small_case(15, 2, H, 1, 400)
+    cache = pk.PackKVCache(B, H, 3, 4, ragged=True, keep_perm=True)
+    oc = O.RaggedOracleCache(2, H, 3, 4)
+    oc.encode_blocks_ragged(k[:, :, :384], v[:, :, :384], 3)
+    for t in range(384, 400):
+        oc.append_token_ragged(k[:, :, t], v[:, :, t], [0] if t >= 390 else None)
+    wide = np.zeros((B, H, 384, 128), np.float16)
+    wide[:2] = k[:, :, :384]
+    kd = to_dev(wide)
+    wide[:2] = v[:, :, :384]
+    pk.packkv_encode_block(cache, kd, to_dev(wide), 3)
+    cache.k_tail[:2] = to_dev(oc.k_tail)
+    cache.v_tail[:2] = to_dev(oc.v_tail)
+    cache.set_lengths([3] * B, [16, 6] + [0] * (B - 2))
+    pk.packkv_fork_sequences(cache, [b % 2 for b in range(2, B)], list(range(2, B)))
+    q = _queries(B, H * rows, rows)
+    out = torch.empty(q.shape, device="cuda")
+    for window, sinks in [(1000, 0), (140, 2)]:
+        pk.packkv_attention_window(cache, to_dev(q), SCALE, out, window, sinks=sinks, queries=queries)
+        got = out.double().cpu().numpy()
+        for b in range(0, B, 2):
+            ref, terms = O.window_attention(oc, q[b:b + 2], SCALE, window, sinks, queries)
+            assert_within_terms(got[b:b + 2], ref, terms, f"sequences {b}, {b + 1}")
+            assert np.linalg.norm(got[b:b + 2] - ref) <= 1e-5 * np.linalg.norm(ref)
+    assert pk.packkv_get_status(cache) == 0
+
+
+def test_long_row_and_empty_caches(pk):
+    cache, oc = _caches(pk, 1, 1, 3, [128 * 30 + 77], 16)
+    _check(pk, cache, oc, 2, 1, 3500, 4, 2)
+    for ragged in (False, True):
+        cache = pk.PackKVCache(2, 2, 1, 4, ragged=ragged, keep_perm=True)
+        out = torch.full((2, 4, 128), 7.0, device="cuda")
+        pk.packkv_attention_window(cache, torch.ones((2, 4, 128), device="cuda").half(), SCALE, out, 5, queries=2)
+        assert torch.all(out == 0)
+
+
+def test_refusals_of_the_binding(pk):
+    cache = pk.PackKVCache(1, 1, 1, 4, keep_perm=True)
+    q = torch.zeros((1, 2, 128), dtype=torch.float16, device="cuda")
+    out = torch.empty((1, 2, 128), device="cuda")
+    for bad in (dict(q=q.float()), dict(q=q[:, :, :64]), dict(out=out[:, :1]), dict(out=out.half()), dict(q=q.cpu()),
+                dict(q=q[0]), dict(ws=torch.empty(16, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            pk.packkv_attention_window(cache, bad.get("q", q), 1.0, bad.get("out", out), 8, ws=bad.get("ws"))
+    with pytest.raises(pk.PackKVError) as e:
+        pk.packkv_attention_window(cache, q, 1.0, out, 8, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == pk.ERR_INVALID_ARG
