@@ -58,7 +58,8 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, int n) {
 
 // Three CTAs per (pair, head): the K tail, the V tail, and the blocks' entries and
 // permutations.
-__global__ void __launch_bounds__(256) fork_kernel(const packkv_cache c, const __grid_constant__ PairPlan plan) {
+template <int N>
+__global__ void __launch_bounds__(256) fork_kernel(const packkv_cache c, const __grid_constant__ PairPlanT<N> plan) {
   const int part = blockIdx.x % 3, ih = blockIdx.x / 3;
   const int i = ih / c.kv_heads, h = ih % c.kv_heads;
   const int src = plan.src[i], dst = plan.dst[i];
@@ -90,7 +91,8 @@ __global__ void __launch_bounds__(256) fork_kernel(const packkv_cache c, const _
   }
 }
 
-__global__ void __launch_bounds__(128) free_kernel(const packkv_cache c, const __grid_constant__ RangePlan plan) {
+template <int N>
+__global__ void __launch_bounds__(128) free_kernel(const packkv_cache c, const __grid_constant__ RangePlanT<N> plan) {
   const int b = blockIdx.x / c.kv_heads, h = blockIdx.x % c.kv_heads;
   const int first = plan.first[b], n = plan.count[b];
   for (int j = threadIdx.x; j < n; j += blockDim.x) {
@@ -145,7 +147,8 @@ struct CompactArgs {
 
 // Source entry e of a tensor: false past the sequence's blocks.  *rec = {offset, length},
 // {0xFFFFFFFF, 0} for a freed or an invalid one (*bad).
-__device__ __forceinline__ bool source_entry(const CompactArgs& a, const LengthPlan& plan, int tensor, int64_t e,
+template <class Plan>
+__device__ __forceinline__ bool source_entry(const CompactArgs& a, const Plan& plan, int tensor, int64_t e,
                                              uint2* rec, long* at, bool* bad) {
   const int row = (int)(e / a.most), j = (int)(e - (int64_t)row * a.most);
   const int b = row / a.src.kv_heads, h = row - b * a.src.kv_heads;
@@ -170,7 +173,8 @@ __device__ __forceinline__ bool source_entry(const CompactArgs& a, const LengthP
   return true;
 }
 
-__global__ void __launch_bounds__(256) mark_kernel(const CompactArgs a, const __grid_constant__ LengthPlan plan) {
+template <int N>
+__global__ void __launch_bounds__(256) mark_kernel(const CompactArgs a, const __grid_constant__ LengthPlanT<N> plan) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (x >= 2 * a.entries) return;
@@ -185,7 +189,8 @@ __global__ void __launch_bounds__(256) mark_kernel(const CompactArgs a, const __
 
 // Whether entry e, record r, is the first that names its record; *first = that entry,
 // -1 if the slot belongs to a record that overlaps r (a corrupt index).
-__device__ __forceinline__ bool owns_record(const CompactArgs& a, const LengthPlan& plan, int tensor, int64_t e,
+template <class Plan>
+__device__ __forceinline__ bool owns_record(const CompactArgs& a, const Plan& plan, int tensor, int64_t e,
                                             const uint2& r, int64_t* first) {
   *first = (int64_t)(uint32_t)~a.ws.owner[tensor][r.x / kMinRecord16];
   if (*first == e) return true;
@@ -200,7 +205,8 @@ __device__ __forceinline__ bool owns_record(const CompactArgs& a, const LengthPl
 constexpr unsigned long long kAggregate = 1ull << 62, kPrefix = 2ull << 62, kValue = (1ull << 62) - 1;
 
 // Exclusive sums of the owned records' lengths: tile `ticket` of tensor blockIdx.y.
-__global__ void __launch_bounds__(kTile) offsets_kernel(const CompactArgs a, const __grid_constant__ LengthPlan plan) {
+template <int N>
+__global__ void __launch_bounds__(kTile) offsets_kernel(const CompactArgs a, const __grid_constant__ LengthPlanT<N> plan) {
   __shared__ uint32_t warp_sums[kTile / 32];
   __shared__ uint32_t my_tile;
   __shared__ unsigned long long before;
@@ -328,8 +334,9 @@ struct Mover {  // lane 0's pipeline: load n goes to stage n % 3, store n - 1 is
   }
 };
 
+template <int N>
 __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const CompactArgs a, uint32_t stage_bytes,
-                                                              const __grid_constant__ LengthPlan plan) {
+                                                              const __grid_constant__ LengthPlanT<N> plan) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t bars[kMoveWarps][kMoveStages];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -433,20 +440,45 @@ cudaError_t sm_count(int* sms) {
 }  // namespace
 
 cudaError_t launch_fork(const packkv_cache& c, const PairPlan& plan, int n, cudaStream_t stream) {
-  fork_kernel<<<(unsigned)(3 * n * c.kv_heads), 256, 0, stream>>>(c, plan);
+  const unsigned grid = (unsigned)(3 * n * c.kv_heads);
+  if (n > kSmallBatch) {
+    fork_kernel<<<grid, 256, 0, stream>>>(c, plan);
+  } else {
+    PairPlanT<kSmallBatch> small;
+    for (int i = 0; i < n; ++i) {
+      small.src[i] = plan.src[i];
+      small.dst[i] = plan.dst[i];
+      small.blocks[i] = plan.blocks[i];
+      small.tail[i] = plan.tail[i];
+    }
+    fork_kernel<<<grid, 256, 0, stream>>>(c, small);
+  }
   return cudaGetLastError();
 }
 
 cudaError_t launch_free(const packkv_cache& c, const RangePlan& plan, int most, cudaStream_t stream) {
   const int threads = most >= 128 ? 128 : (most + 31) / 32 * 32;
-  free_kernel<<<(unsigned)(c.batch * c.kv_heads), threads, 0, stream>>>(c, plan);
+  const unsigned grid = (unsigned)(c.batch * c.kv_heads);
+  if (c.batch > kSmallBatch) {
+    free_kernel<<<grid, threads, 0, stream>>>(c, plan);
+  } else {
+    RangePlanT<kSmallBatch> small;
+    for (int b = 0; b < c.batch; ++b) {
+      small.first[b] = plan.first[b];
+      small.count[b] = plan.count[b];
+    }
+    free_kernel<<<grid, threads, 0, stream>>>(c, small);
+  }
   return cudaGetLastError();
 }
 
 size_t compact_workspace_bytes(int64_t entries, uint64_t arena16) { return compact_ws(nullptr, entries, arena16).bytes; }
 
-cudaError_t launch_compact(const packkv_cache& dst, const packkv_cache& src, const LengthPlan& plan, int most, void* ws,
-                           cudaStream_t stream) {
+namespace {
+
+template <int N>
+cudaError_t compact_with(const packkv_cache& dst, const packkv_cache& src, const LengthPlanT<N>& plan, int most,
+                         void* ws, cudaStream_t stream) {
   CompactArgs a{};
   a.dst = dst;
   a.src = src;
@@ -468,20 +500,33 @@ cudaError_t launch_compact(const packkv_cache& dst, const packkv_cache& src, con
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, &offsets_kernel, a, plan);
+  e = cudaLaunchKernelEx(&cfg, &offsets_kernel<N>, a, plan);
   if (e != cudaSuccess) return e;
   int sms = 148;
   e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const uint32_t stage = (uint32_t)raw_record_bytes((int)src.fmt.bits);
   const size_t smem = (size_t)kMoveWarps * kMoveStages * stage;
-  e = cudaFuncSetAttribute(&move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveWarps * kMoveStages * 8720);
+  e = cudaFuncSetAttribute(&move_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveWarps * kMoveStages * 8720);
   if (e != cudaSuccess) return e;
   const int64_t tasks = (a.entries + kBatch - 1) / kBatch, want = (tasks + kMoveWarps - 1) / kMoveWarps;
   cfg.gridDim = dim3((unsigned)(want < 2L * sms ? want : 2L * sms));
   cfg.blockDim = dim3(kMoveWarps * 32);
   cfg.dynamicSmemBytes = smem;
-  return cudaLaunchKernelEx(&cfg, &move_kernel, a, stage, plan);
+  return cudaLaunchKernelEx(&cfg, &move_kernel<N>, a, stage, plan);
+}
+
+}  // namespace
+
+cudaError_t launch_compact(const packkv_cache& dst, const packkv_cache& src, const LengthPlan& plan, int most, void* ws,
+                           cudaStream_t stream) {
+  if (src.batch > kSmallBatch) return compact_with(dst, src, plan, most, ws, stream);
+  LengthPlanT<kSmallBatch> small;
+  for (int b = 0; b < src.batch; ++b) {
+    small.blocks[b] = plan.blocks[b];
+    small.tail[b] = plan.tail[b];
+  }
+  return compact_with(dst, src, small, most, ws, stream);
 }
 
 }  // namespace packkv

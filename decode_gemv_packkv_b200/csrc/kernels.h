@@ -135,27 +135,38 @@ struct HeadsArgs {
   packkv_rope rope;
 };
 // Tokens each sequence of a ragged batch holds (0xFFFFFFFF: it takes no token).
-struct RaggedLengths {
-  uint32_t tokens[kMaxRaggedBatch];
+template <int N>
+struct RaggedLengthsT {
+  uint32_t tokens[N];
 };
+using RaggedLengths = RaggedLengthsT<kMaxRaggedBatch>;
 cudaError_t launch_prompt_heads(const HeadsArgs& a, cudaStream_t stream);
 // `tokens` held by every sequence, or the lengths of a ragged batch.
 cudaError_t launch_append_heads(const HeadsArgs& a, uint32_t tokens, const RaggedLengths* lengths,
                                 cudaStream_t stream);
 
-// The blocks of a cache (blocks.cu).  Per-sequence arguments travel by value.
-struct PairPlan {  // sequence dst[i] becomes src[i], which holds blocks[i] blocks and tail[i] tail tokens
-  int16_t src[kMaxRaggedBatch], dst[kMaxRaggedBatch];
-  int32_t blocks[kMaxRaggedBatch];
-  uint8_t tail[kMaxRaggedBatch];
+// The blocks of a cache (blocks.cu).  Per-sequence arguments travel by value, like those
+// above; calls of at most kSmallBatch sequences (or pairs) take plans of that size, because
+// a launch copies its parameters (16 KB of them took the call from 2.3 to 3.9 us).
+constexpr int kSmallBatch = 64;
+template <int N>
+struct PairPlanT {  // sequence dst[i] becomes src[i], which holds blocks[i] blocks and tail[i] tail tokens
+  int16_t src[N], dst[N];
+  int32_t blocks[N];
+  uint8_t tail[N];
 };
-struct RangePlan {  // logical blocks [first, first + count) of every sequence
-  int32_t first[kMaxRaggedBatch], count[kMaxRaggedBatch];
+template <int N>
+struct RangePlanT {  // logical blocks [first, first + count) of every sequence
+  int32_t first[N], count[N];
 };
-struct LengthPlan {  // what every sequence holds
-  int32_t blocks[kMaxRaggedBatch];
-  uint8_t tail[kMaxRaggedBatch];
+template <int N>
+struct LengthPlanT {  // what every sequence holds
+  int32_t blocks[N];
+  uint8_t tail[N];
 };
+using PairPlan = PairPlanT<kMaxRaggedBatch>;
+using RangePlan = RangePlanT<kMaxRaggedBatch>;
+using LengthPlan = LengthPlanT<kMaxRaggedBatch>;
 cudaError_t launch_fork(const packkv_cache& c, const PairPlan& plan, int n, cudaStream_t stream);
 cudaError_t launch_free(const packkv_cache& c, const RangePlan& plan, int most, cudaStream_t stream);
 size_t compact_workspace_bytes(int64_t entries, uint64_t arena16);
@@ -187,13 +198,15 @@ struct WindowArgs {
   float* out;
   float* partials;
 };
-struct WindowPlan {  // ragged batches: what every sequence holds, and its rows' first item
-  int32_t blocks[kMaxRaggedBatch];
-  int32_t base[kMaxRaggedBatch + 1];  // items of the (row, chunk)s of the sequences before
-  uint8_t tail[kMaxRaggedBatch];
+template <int N>
+struct WindowPlanT {  // ragged batches: what every sequence holds, and its rows' first item
+  int32_t blocks[N];
+  int32_t base[N + 1];  // items of the (row, chunk)s of the sequences before
+  uint8_t tail[N];
 };
+using WindowPlan = WindowPlanT<kMaxRaggedBatch>;
 size_t window_workspace_bytes(int batch, int kv_heads, int rows);
 // plan: blocks and tail of every sequence filled in (ragged batches), or NULL
-cudaError_t launch_window(WindowArgs a, WindowPlan* plan, cudaStream_t stream);
+cudaError_t launch_window(WindowArgs a, const WindowPlan* plan, cudaStream_t stream);
 
 }  // namespace packkv

@@ -276,7 +276,10 @@ struct UniformLength {
 // Tokens sequence b holds (kNoToken: it takes none).
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t length_of(const UniformLength& p, int) { return p.tokens; }
-__device__ __forceinline__ uint32_t length_of(const RaggedLengths& p, int b) { return p.tokens[b]; }
+template <int N>
+__device__ __forceinline__ uint32_t length_of(const RaggedLengthsT<N>& p, int b) {
+  return p.tokens[b];
+}
 
 template <class T, bool kHalf, bool kWide, class Plan>
 __global__ void __launch_bounds__(kThreads, !kWide ? 1 : (sizeof(T) == 2 ? 8 : 4)) heads_kernel(const HeadsArgs a, const __grid_constant__ Plan plan) {
@@ -420,7 +423,12 @@ cudaError_t launch_prompt_heads(const HeadsArgs& args, cudaStream_t stream) {
 
 cudaError_t launch_append_heads(const HeadsArgs& a, uint32_t tokens, const RaggedLengths* lengths,
                                 cudaStream_t stream) {
-  if (lengths != nullptr) return launch_heads_p(a, *lengths, stream);
+  if (lengths != nullptr && a.batch > kSmallBatch) return launch_heads_p(a, *lengths, stream);
+  if (lengths != nullptr) {
+    RaggedLengthsT<kSmallBatch> small;
+    for (int b = 0; b < a.batch; ++b) small.tokens[b] = lengths->tokens[b];
+    return launch_heads_p(a, small, stream);
+  }
   return launch_heads_p(a, UniformLength{tokens}, stream);
 }
 

@@ -13,6 +13,7 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <cstring>
 #include <mutex>
 #include <type_traits>
 #include <unordered_map>
@@ -65,6 +66,9 @@ __device__ __forceinline__ float4 param4(const unsigned char* st, int at, int la
   return make_float4(x.x, x.y, y.x, y.y);
 }
 
+template <class Plan>
+constexpr bool kRagged = !std::is_same<Plan, NoPlan>::value;
+
 // A place in the list of all items: (sequence, kv head, chunk of 8 query rows), item.
 struct ItemCursor {
   int b, h, chunk, i;
@@ -78,7 +82,8 @@ struct ItemCursor {
 __device__ __forceinline__ ItemList row_list(const WindowArgs& a, const NoPlan&, int) {
   return item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len);
 }
-__device__ __forceinline__ ItemList row_list(const WindowArgs& a, const WindowPlan& p, int b) {
+template <int N>
+__device__ __forceinline__ ItemList row_list(const WindowArgs& a, const WindowPlanT<N>& p, int b) {
   return item_list(a.queries, a.window, a.sinks, p.blocks[b], p.tail[b]);
 }
 
@@ -87,7 +92,7 @@ template <class Plan>
 __device__ __forceinline__ ItemCursor item_at(const WindowArgs& a, const Plan& p, int chunks, long x) {
   ItemCursor c;
   const int rpc = a.kv_heads * chunks;  // (row, chunk)s of a sequence
-  if constexpr (std::is_same<Plan, WindowPlan>::value) {
+  if constexpr (kRagged<Plan>) {
     int lo = 0, hi = a.batch;  // the last sequence whose first item is <= x has items
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -117,7 +122,7 @@ __device__ __forceinline__ void item_next(const WindowArgs& a, const Plan& p, in
   if (++c.h < a.kv_heads) return;
   c.h = 0;
   ++c.b;
-  if constexpr (std::is_same<Plan, WindowPlan>::value) {  // the next sequence that has items
+  if constexpr (kRagged<Plan>) {  // the next sequence that has items
     while (c.b < a.batch && p.base[c.b + 1] == p.base[c.b]) ++c.b;
     if (c.b < a.batch) c.items = row_list(a, p, c.b);
   }
@@ -809,7 +814,7 @@ __global__ void __launch_bounds__(128) window_merge_kernel(const WindowArgs a, i
     return;
   }
   long first;
-  if constexpr (std::is_same<Plan, WindowPlan>::value)
+  if constexpr (kRagged<Plan>)
     first = plan.base[b] + (bhc - (long)b * rpc) * items.n;
   else
     first = bhc * items.n;
@@ -971,7 +976,7 @@ cudaError_t clusters(WindowArgs a, const Plan& plan, int g, const WinKernel& k, 
 template <class Plan>
 cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
   long per_head = 0;  // items of one kv head over all sequences
-  if constexpr (std::is_same<Plan, WindowPlan>::value) {
+  if constexpr (kRagged<Plan>) {
     for (int b = 0; b < a.batch; ++b) {
       const int n = item_list(a.queries, a.window, a.sinks, plan.blocks[b], plan.tail[b]).n;
       if (n > a.most_items) a.most_items = n;
@@ -1005,7 +1010,7 @@ cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
   cluster = cluster || 2 * items(g) <= (long)ctas * kWinWarps;
   a.n_items = items(g);
   if (a.n_items > 0x7fffffffL) return cudaErrorInvalidValue;
-  if constexpr (std::is_same<Plan, WindowPlan>::value) {
+  if constexpr (kRagged<Plan>) {
     long at = 0;
     for (int b = 0; b < a.batch; ++b) {
       plan.base[b] = (int32_t)at;
@@ -1027,10 +1032,21 @@ size_t window_workspace_bytes(int batch, int kv_heads, int rows) {
   return ((size_t)max_parts() * (rows < 4 ? rows : 4) + (size_t)batch * kv_heads * rows) * kPartFloats * sizeof(float);
 }
 
-cudaError_t launch_window(WindowArgs a, WindowPlan* plan, cudaStream_t stream) {
-  if (plan != nullptr) return launch_window_p<WindowPlan>(a, *plan, stream);
+cudaError_t launch_window(WindowArgs a, const WindowPlan* plan, cudaStream_t stream) {
+  if (plan != nullptr && a.batch > kSmallBatch) {
+    thread_local WindowPlan p;
+    std::memcpy(p.blocks, plan->blocks, sizeof(int32_t) * a.batch);
+    std::memcpy(p.tail, plan->tail, a.batch);
+    return launch_window_p(a, p, stream);
+  }
+  if (plan != nullptr) {
+    WindowPlanT<kSmallBatch> p;
+    std::memcpy(p.blocks, plan->blocks, sizeof(int32_t) * a.batch);
+    std::memcpy(p.tail, plan->tail, a.batch);
+    return launch_window_p(a, p, stream);
+  }
   NoPlan none;
-  return launch_window_p<NoPlan>(a, none, stream);
+  return launch_window_p(a, none, stream);
 }
 
 }  // namespace packkv

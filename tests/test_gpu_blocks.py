@@ -181,11 +181,16 @@ def test_compact_capacity_and_bad_entries(pk):
 
 def test_many_tiles(pk):
     """More entries than one look-back tile, most of them short sequences."""
-    src = _filled(pk, 40, 4, 20, 2, [128 * (1 + b % 20) for b in range(40)], 6)
-    pk.packkv_free_blocks(src, [0] * 40, [b % 3 if b % 20 >= 2 else 0 for b in range(40)])
-    dst = pk.PackKVCache(40, 4, 20, 2, ragged=True, keep_perm=True)
+    B = 70                                   # past the small plans of 64 sequences
+    src = _filled(pk, B, 2, 20, 2, [128 * (1 + b % 20) for b in range(B)], 6)
+    pk.packkv_free_blocks(src, [0] * B, [b % 3 if b % 20 >= 2 else 0 for b in range(B)])
+    dst = pk.PackKVCache(B, 2, 20, 2, ragged=True, keep_perm=True)
     pk.packkv_compact(dst, src)
     _check_compacted(pk, dst, src)
+    before = dst.k_index.clone()
+    pk.packkv_fork_sequences(dst, [19] * 66, [b for b in range(B) if b not in (0, 19, 68, 69)])
+    assert torch.equal(dst.k_index[67], before[19]) and torch.equal(dst.k_index[68], before[68])
+    assert dst.seq_blocks[5] == 20 and dst.seq_blocks[0] == 1
 
 
 def test_serving_loop(pk):

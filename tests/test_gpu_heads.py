@@ -191,6 +191,30 @@ def test_append_norm_rope_grows_the_cache(pk, ragged):
     assert pk.packkv_get_status(a) == 0
 
 
+def test_append_to_many_ragged_sequences(pk):
+    B = 70                                   # past the small plans of 64 sequences
+    x, _, _ = _inputs(B, 1, 1, 1, "fp32", 4)
+    d = x[:, 0].cuda()
+    cache = pk.PackKVCache(B, 1, 3, 4, ragged=True)
+    held = [(17 * b) % 300 for b in range(B)]
+    cache.set_lengths([t // 128 for t in held], [t % 128 for t in held])
+    on = [b % 5 != 3 for b in range(B)]
+    q_out = torch.zeros((B, 1, 128), dtype=torch.float16, device="cuda")
+    rope = pk.Rope()
+    pk.packkv_append_norm_rope(cache, rope, d[:, :1], d[:, 1:2], d[:, 2:], q_out, active=on)
+    want = [torch.empty((B, 1, 1, 128), dtype=torch.float16, device="cuda") for _ in range(3)]
+    pos = torch.tensor(held, dtype=torch.int32, device="cuda")[:, None]
+    pk.packkv_norm_rope(rope, d[:, None, :1], d[:, None, 1:2], d[:, None, 2:], *want, positions=pos)
+    for b in range(B):
+        if on[b]:
+            assert torch.equal(q_out[b], want[0][b, :, 0])
+            assert torch.equal(cache.k_tail[b, :, held[b] % 128], want[1][b, :, 0])
+        else:
+            assert torch.all(q_out[b] == 0) and torch.all(cache.k_tail[b] == 0)
+    grown = [128 * n + t for n, t in zip(cache.seq_blocks, cache.seq_tail)]
+    assert grown == [h + o for h, o in zip(held, on)]
+
+
 def test_append_in_a_graph(pk):
     """Captured and replayed with other inputs: the position is the captured one, the tail
     slot takes the new token."""

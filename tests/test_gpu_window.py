@@ -207,9 +207,9 @@ def test_repeatable_and_in_a_graph(pk):
 
 @pytest.mark.parametrize("rows,queries", [(1, 1), (2, 2), (4, 1), (8, 4)])
 def test_many_sequences(pk, rows, queries):
-    """More items than half the device's warps (the even split): 64 sequences forked from two,
+    """More items than half the device's warps (the even split): 72 sequences forked from two,
     every one with queries of its own."""
-    B, H = 64, 8
+    B, H = 72, 8
     k, v, _ = synth.small_case(15, 2, H, 1, 400)
     cache = pk.PackKVCache(B, H, 3, 4, ragged=True, keep_perm=True)
     oc = O.RaggedOracleCache(2, H, 3, 4)
