@@ -16,6 +16,8 @@
 // stores, four in flight, took 151.
 // Forks and frees are a few entries per block: bound by the launch.  Three CTAs per (pair,
 // head), four loads in flight: 32 pairs x 8 heads of 64 blocks in 3.7 us (6.9 with one CTA).
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -435,11 +437,22 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const CompactArgs
   if (lane == 0) mv.finish();
 }
 
-cudaError_t sm_count(int* sms) {
+// SMs of the current device; the first time there, raises the move kernels' shared memory limit.
+cudaError_t move_configure(int* sms) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (dev < kMaxDevices && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  const int smem = kMoveWarps * kMoveStages * raw_record_bytes(4);
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(&move_kernel<kSmallBatch>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(&move_kernel<kMaxRaggedBatch>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev < kMaxDevices) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace
@@ -490,7 +503,9 @@ cudaError_t compact_with(const packkv_cache& dst, const packkv_cache& src, const
   a.most = most > 0 ? most : 1;
   a.entries = (int64_t)src.batch * src.kv_heads * a.most;
   a.ws = compact_ws(ws, a.entries, src.arena_bytes / 16);
-  cudaError_t e = cudaMemsetAsync(ws, 0, a.ws.clear_bytes, stream);
+  int sms = 0;
+  cudaError_t e = move_configure(&sms);
+  if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0, a.ws.clear_bytes, stream);
   if (e != cudaSuccess) return e;
   mark_kernel<<<(unsigned)((2 * a.entries + 255) / 256), 256, 0, stream>>>(a, plan);
   e = cudaGetLastError();
@@ -507,13 +522,8 @@ cudaError_t compact_with(const packkv_cache& dst, const packkv_cache& src, const
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, &offsets_kernel<N>, a, plan);
   if (e != cudaSuccess) return e;
-  int sms = 148;
-  e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
   const uint32_t stage = (uint32_t)raw_record_bytes((int)src.fmt.bits);
   const size_t smem = (size_t)kMoveWarps * kMoveStages * stage;
-  e = cudaFuncSetAttribute(&move_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveWarps * kMoveStages * 8720);
-  if (e != cudaSuccess) return e;
   const int64_t tasks = (a.entries + kBatch - 1) / kBatch, want = (tasks + kMoveWarps - 1) / kMoveWarps;
   cfg.gridDim = dim3((unsigned)(want < 2L * sms ? want : 2L * sms));
   cfg.blockDim = dim3(kMoveWarps * 32);

@@ -21,10 +21,9 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstring>
-#include <mutex>
 #include <type_traits>
-#include <unordered_map>
 
 #include "decode.cuh"
 
@@ -880,44 +879,43 @@ __global__ void __launch_bounds__(128) window_merge_kernel(const WindowArgs a, i
 struct WinKernel {
   const void* fn;
   int smem;
+  std::atomic<int>* ctas;  // [kMaxDevices]: CTAs of the kernel a device holds (0: not asked yet)
 };
 
-template <class Plan>
-WinKernel win_select(int bits, int g, bool even) {
-#define PACKKV_WCASE(B, GG)                                                                                         \
-  if (bits == B && g == GG)                                                                                         \
-    return even ? WinKernel{reinterpret_cast<const void*>(&window_kernel<B, GG, true, Plan>),                       \
-                            kWinWarps * WinCfg<B, GG, true>::kWarpSmem}                                             \
-                : WinKernel{reinterpret_cast<const void*>(&window_kernel<B, GG, false, Plan>),                      \
-                            kWinWarps * WinCfg<B, GG, false>::kWarpSmem};
-  PACKKV_WCASE(4, 1) PACKKV_WCASE(4, 2) PACKKV_WCASE(4, 4)
-  PACKKV_WCASE(3, 1) PACKKV_WCASE(3, 2) PACKKV_WCASE(3, 4)
-  PACKKV_WCASE(2, 1) PACKKV_WCASE(2, 2) PACKKV_WCASE(2, 4)
-#undef PACKKV_WCASE
-  return {nullptr, 0};
+constexpr int kMaxDevices = 64;
+
+template <int BITS, int G, bool kEven, class Plan>
+WinKernel win_kernel() {
+  static std::atomic<int> ctas[kMaxDevices];
+  return {reinterpret_cast<const void*>(&window_kernel<BITS, G, kEven, Plan>),
+          kWinWarps * WinCfg<BITS, G, kEven>::kWarpSmem, ctas};
 }
 
-// Raises the kernel's shared memory limit once per device; CTAs that the device holds.
-cudaError_t win_configure(const WinKernel& k, int* ctas) {
-  static std::mutex mu;
-  static std::unordered_map<long long, int> done;
-  int dev = 0, sms = 0, per_sm = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const long long key = (long long)(reinterpret_cast<uintptr_t>(k.fn)) * 64 + dev;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = done.find(key);
-  if (it != done.end()) {
-    *ctas = it->second;
-    return cudaSuccess;
-  }
-  e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+// bits 2..4, g 1, 2 or 4.
+template <class Plan>
+WinKernel win_select(int bits, int g, bool even) {
+#define PACKKV_WCASE(B, GG) \
+  if (bits == B && g == GG) return even ? win_kernel<B, GG, true, Plan>() : win_kernel<B, GG, false, Plan>();
+  PACKKV_WCASE(4, 1) PACKKV_WCASE(4, 2) PACKKV_WCASE(4, 4)
+  PACKKV_WCASE(3, 1) PACKKV_WCASE(3, 2) PACKKV_WCASE(3, 4)
+  PACKKV_WCASE(2, 1) PACKKV_WCASE(2, 2)
+#undef PACKKV_WCASE
+  return even ? win_kernel<2, 4, true, Plan>() : win_kernel<2, 4, false, Plan>();
+}
+
+// CTAs of the kernel that the current device holds; raises its shared memory limit there
+// the first time.
+cudaError_t win_configure(const WinKernel& k, int dev, int* ctas) {
+  if (dev < kMaxDevices && (*ctas = k.ctas[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  int sms = 0, per_sm = 0;
+  cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess)
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, kWinWarps * 32, (size_t)k.smem);
   if (e != cudaSuccess) return e;
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  done[key] = *ctas = sms * per_sm;
+  *ctas = sms * per_sm;
+  if (dev < kMaxDevices) k.ctas[dev].store(*ctas, std::memory_order_relaxed);
   return cudaSuccess;
 }
 
@@ -1005,7 +1003,7 @@ cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
     g = 1;
     cluster = true;
   } else if (a.rows >= 2) {
-    e = win_configure(win_select<Plan>(a.bits, 2, true), &ctas);
+    e = win_configure(win_select<Plan>(a.bits, 2, true), dev, &ctas);
     if (e != cudaSuccess) return e;
     if (2 * items(2) <= (long)ctas * kWinWarps) {
       g = 2;
@@ -1013,7 +1011,7 @@ cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
     }
   }
   const WinKernel even = win_select<Plan>(a.bits, g, true);
-  e = win_configure(even, &ctas);
+  e = win_configure(even, dev, &ctas);
   if (e != cudaSuccess) return e;
   cluster = cluster || 2 * items(g) <= (long)ctas * kWinWarps;
   a.n_items = items(g);
@@ -1028,7 +1026,7 @@ cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
   }
   if (!cluster) return even_split(a, plan, g, even, ctas * kWinWarps, stream);
   const WinKernel k = win_select<Plan>(a.bits, g, false);
-  e = win_configure(k, &ctas);
+  e = win_configure(k, dev, &ctas);
   if (e != cudaSuccess) return e;
   return clusters(a, plan, g, k, ctas, stream);
 }

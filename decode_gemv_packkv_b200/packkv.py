@@ -41,6 +41,7 @@ EXPORTED = [
 ]
 
 RAGGED_MAX_BATCH = 2048
+_INT_MAX = (1 << 31) - 1
 
 DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}  # PACKKV_DTYPE_*
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1                                # which channels form a pair
@@ -385,52 +386,49 @@ class Rope:
 
 # packkv_heads: dtype, q_heads, kv_heads, eps, the rows of q, k, v, q_weight, k_weight
 _HEADS = struct.Struct("=iiif QqqqQqqqQqqq QQ")
-_NO_ROWS = (0, 0, 0, 0)
-
-
-def _rows(name, x, like, dims):
-    """The packkv_rows of a [batch, tokens, heads, 128] (or [batch, heads, 128]) tensor."""
-    if x is None:
-        return _NO_ROWS
-    shape, stride = x.shape, x.stride()
-    if len(shape) != dims or shape[-1] != HEAD_DIM or stride[-1] != 1:
-        raise ValueError(f"{name} must have {dims} dimensions, the last one {HEAD_DIM} contiguous channels")
-    if x is not like and (shape[:-2] != like.shape[:-2] or x.dtype != like.dtype or x.get_device() != like.get_device()):
-        raise ValueError(f"{name} must have the batch, tokens, dtype and device of the others")
-    return (x.data_ptr(), stride[0], stride[1] if dims == 4 else 0, stride[-2])
-
-
-def _weight(name, w, x, like):
-    if w is None:
-        return 0
-    if (x is None or w.dtype != torch.float32 or w.shape != (HEAD_DIM,) or w.stride(0) != 1
-            or w.get_device() != like.get_device()):
-        raise ValueError(f"{name} must be a contiguous fp32 [{HEAD_DIM}] on the heads' device, for heads that are given")
-    return w.data_ptr()
 
 
 def _heads(q, k, v, q_weight, k_weight, eps, dims):
-    """The packkv_heads of q, k, v: CUDA tensors of any strides, channels contiguous."""
+    """The packkv_heads of q, k, v ([batch, tokens, heads, 128] or [batch, heads, 128] CUDA
+    tensors of any strides, channels contiguous), and the first of them."""
     like = q if q is not None else k
     if like is None or (k is None) != (v is None):
         raise ValueError("expected q, or k and v, or all three")
-    dtype = DTYPES.get(like.dtype)
-    if dtype is None or not like.is_cuda:
+    kind, at, shape = like.dtype, like.get_device(), like.shape
+    dtype, lead = DTYPES.get(kind), shape[:-2]
+    if dtype is None or at < 0:
         raise ValueError("q, k, v must be fp16, bf16 or fp32 CUDA tensors")
+    heads, rows = [0, 0, 0], []
+    for i, x in enumerate((q, k, v)):
+        if x is None:
+            rows += (0, 0, 0, 0)
+            continue
+        stride = x.stride()
+        if x is not like:
+            shape = x.shape
+            if shape[:-2] != lead or x.dtype != kind or x.get_device() != at:
+                raise ValueError("q, k, v must have the same batch, tokens, dtype and device")
+        if len(shape) != dims or shape[-1] != HEAD_DIM or stride[-1] != 1:
+            raise ValueError(f"q, k, v must have {dims} dimensions, the last one {HEAD_DIM} contiguous channels")
+        heads[i] = shape[-2]
+        rows += (x.data_ptr(), stride[0], stride[1] if dims == 4 else 0, stride[-2])
+    if heads[1] != heads[2]:
+        raise ValueError("k and v must have the same heads")
     if eps is None:
         if q_weight is not None or k_weight is not None:
             raise ValueError("weights need eps (a norm)")
-        eps = -1.0
-    elif not eps >= 0:
+        return _HEADS.pack(dtype, heads[0], heads[1], -1.0, *rows, 0, 0), like
+    if not eps >= 0:
         raise ValueError("eps must be >= 0 (None: no norm)")
-    rows = _rows("q", q, like, dims) + _rows("k", k, like, dims) + _rows("v", v, like, dims)
-    hk = 0
-    if k is not None:
-        hk = k.shape[-2]
-        if v.shape[-2] != hk:
-            raise ValueError("k and v must have the same heads")
-    return _HEADS.pack(dtype, 0 if q is None else q.shape[-2], hk, eps, *rows, _weight("q_weight", q_weight, q, like),
-                       _weight("k_weight", k_weight, k, like)), like
+    weights = []
+    for w, x in ((q_weight, q), (k_weight, k)):
+        if w is None:
+            weights.append(0)
+            continue
+        if x is None or w.dtype != torch.float32 or w.shape != (HEAD_DIM,) or w.stride(0) != 1 or w.get_device() != at:
+            raise ValueError(f"a weight must be a contiguous fp32 [{HEAD_DIM}] on the device of heads that are given")
+        weights.append(w.data_ptr())
+    return _HEADS.pack(dtype, heads[0], heads[1], eps, *rows, *weights), like
 
 
 def _stream_of(t: torch.Tensor, stream):
@@ -509,8 +507,10 @@ def packkv_attention_window(cache: PackKVCache, q: torch.Tensor, scale: float, o
         raise ValueError("q must be fp16 [batch, q_heads, 128] on the cache's device")
     if ws is None:
         ws = cache.window_workspace(shape[1])
+    # no sequence has more than 2^31 tokens: larger limits mean the same
+    window, sinks = min(window, _INT_MAX), min(sinks, _INT_MAX)
     status = _lib.packkv_attention_window(cache.addr, _out_ptr("q", q, torch.float16, shape, at), shape[1], queries,
-                                          window, sinks, scale, _out_ptr("out", out, torch.float32, shape, at),
+                                          window, sinks, float(scale), _out_ptr("out", out, torch.float32, shape, at),
                                           _ws_ptr(ws, at), ws.nbytes, _stream_of(q, stream))
     if status:
         _check("packkv_attention_window", status)

@@ -109,6 +109,21 @@ def test_positions_from_first(pk, first):
         assert np.all(err <= np.maximum(np.abs(ref) * 2.0 ** -11, 2.0 ** -25) * (1 + 2.0 ** -10) + N * 2.0 ** -20)
 
 
+def test_keys_alone_and_several_launch_shapes(pk):
+    """k and v without q; prompts short and long enough for every number of tokens per CTA
+    give the same bits per token."""
+    rope = pk.Rope(128, pk.ROPE_HALF)
+    B, T, h = 2, 1800, 3
+    x = torch.randn(B, T, 2 * h, 128, device="cuda").half()
+    full = [torch.empty((B, h, T, 128), dtype=torch.float16, device="cuda") for _ in range(2)]
+    pk.packkv_norm_rope(rope, None, x[:, :, :h], x[:, :, h:], None, *full, eps=1e-6, first=7)
+    assert torch.equal(full[1], x[:, :, h:].transpose(1, 2))
+    for t0, t1 in ((0, 1), (5, 105), (900, 1250)):
+        part = [torch.empty((B, h, t1 - t0, 128), dtype=torch.float16, device="cuda") for _ in range(2)]
+        pk.packkv_norm_rope(rope, None, x[:, t0:t1, :h], x[:, t0:t1, h:], None, *part, eps=1e-6, first=7 + t0)
+        assert torch.equal(part[0], full[0][:, :, t0:t1]) and torch.equal(part[1], full[1][:, :, t0:t1])
+
+
 def test_strides_and_unaligned_rows(pk):
     """Head-major rows, a batch stride of its own, and data that starts one element off a
     vector: the same bits as from the fused projection."""

@@ -93,7 +93,7 @@ def test_borders_of_tail_and_window(pk, tokens):
 def test_large_limits(pk):
     cache, oc = _caches(pk, 2, 1, 2, [300, 70], 3)
     big = (1 << 31) - 1
-    for window, sinks in [(big, 0), (1, big), (big, big)]:
+    for window, sinks in [(big, 0), (1, big), (big, big), (1 << 40, 1 << 33)]:
         _check(pk, cache, oc, 1, 1, window, sinks, 1)
         _check(pk, cache, oc, 8, 8, window, sinks, 2)
 
@@ -234,6 +234,16 @@ def test_many_sequences(pk, rows, queries):
             ref, terms = O.window_attention(oc, q[b:b + 2], SCALE, window, sinks, queries)
             assert_within_terms(got[b:b + 2], ref, terms, f"sequences {b}, {b + 1}")
             assert np.linalg.norm(got[b:b + 2] - ref) <= 1e-5 * np.linalg.norm(ref)
+    want = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    qd = to_dev(q)
+    with torch.cuda.graph(graph):
+        pk.packkv_attention_window(cache, qd, SCALE, out, window, sinks=sinks, queries=queries)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
     assert pk.packkv_get_status(cache) == 0
 
 
