@@ -75,8 +75,9 @@ __device__ __forceinline__ uint2 half4(const float (&y)[4]) {
 }
 
 // The channels of a lane and how its pairs turn.  Wide (vector accesses): ca + i and
-// cb + i, i < 4.  Narrow (half layouts whose rot_dim is no multiple of 8, and unaligned
-// rows): element i at channels ca_i and cb_i.
+// cb + i, i < 4.  Narrow (unaligned rows): element i at channels ca_i and cb_i.  Half
+// layouts whose rot_dim is no multiple of 8 cannot have both members of every pair at
+// aligned places of one lane: they swap members through shared memory (kSwap).
 struct LaneMap {
   int ca[4], cb[4];
   int pa[4], pb[4];  // pair of element i of A and of B
@@ -84,12 +85,17 @@ struct LaneMap {
 
 // Layout of lane l (0..15).  half: (A_i, B_i) is pair pa[i]; interleaved: (A_0, A_1),
 // (A_2, A_3), (B_0, B_1), (B_2, B_3) are pairs.
-template <bool kHalf, bool kWide>
+template <bool kHalf, bool kWide, bool kSwap>
 __device__ __forceinline__ LaneMap lane_map(int rot, int l) {
   LaneMap m;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (!kHalf) {
+    if constexpr (kSwap) {
+      m.ca[i] = 4 * l + i;
+      m.cb[i] = 64 + 4 * l + i;
+      m.pa[i] = m.ca[i] < rot / 2 ? m.ca[i] : m.ca[i] - rot / 2;
+      m.pb[i] = m.cb[i] < rot / 2 ? m.cb[i] : m.cb[i] - rot / 2;
+    } else if constexpr (!kHalf) {
       m.ca[i] = 4 * l + i;
       m.cb[i] = 64 + 4 * l + i;
       m.pa[i] = 2 * l + (i >> 1);
@@ -174,13 +180,35 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const HeadRow& r, const
 // infinity would spoil its neighbour).
 struct Turn {
   float2 ca[2], sa[2], cb[2], sb[2];
-  uint32_t on;  // half: bit 0 (all four pairs); interleaved: bits 0, 1 (A), 2, 3 (B)
+  uint32_t on;  // half: bit i (pair i); interleaved: bits 0, 1 (A), 2, 3 (B); swapped: a bit per channel
 };
 
-template <bool kHalf, bool kWide>
-__device__ __forceinline__ Turn lane_turn(const float2* cs, const HeadRow& w, const LaneMap& m, int rot) {
+template <bool kHalf, bool kWide, bool kSwap>
+__device__ __forceinline__ Turn lane_turn(const float2* cs, const HeadRow& w, const float* weight, const LaneMap& m,
+                                          int rot) {
   Turn u;
   u.on = 0u;
+  if constexpr (kSwap) {  // x' = x c + y s with the other member y of the pair, weights folded in
+    float* c[2] = {&u.ca[0].x, &u.cb[0].x};
+    float* z[2] = {&u.sa[0].x, &u.sb[0].x};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ch = k ? m.cb[i] : m.ca[i], pair = k ? m.pb[i] : m.pa[i];
+        c[k][i] = k ? w.b[i] : w.a[i];
+        z[k][i] = 0.f;
+        if (ch < rot) {
+          const float2 t = cs[pair];
+          const bool first = ch < rot / 2;
+          const float wy = weight ? weight[first ? ch + rot / 2 : ch - rot / 2] : 1.f;
+          c[k][i] *= t.x;
+          z[k][i] = (first ? -t.y : t.y) * wy;
+          u.on |= 1u << (4 * k + i);
+        }
+      }
+    return u;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float ca = w.a[i], sa = 0.f, cb = w.b[i], sb = 0.f;
@@ -218,9 +246,15 @@ __device__ __forceinline__ Turn lane_turn(const float2* cs, const HeadRow& w, co
   return u;
 }
 
-// Norm and rotation of one row.
-template <bool kHalf, bool kWide>
-__device__ __forceinline__ void turn_row(HeadRow& r, bool norm, float eps, const Turn& u) {
+// Place of channel c in a half-warp's swap row: a word of padding per 32, so that lanes four
+// channels apart meet different banks.
+__device__ __forceinline__ int swap_at(int c) { return c + (c >> 5); }
+constexpr int kSwapRow = 133;  // 131 words used; a half-warp has two rows: its neighbour lies 10 banks on
+
+// Norm and rotation of one row.  swap (kSwap): the half-warp's swap row.
+template <bool kHalf, bool kWide, bool kSwap>
+__device__ __forceinline__ void turn_row(HeadRow& r, bool norm, float eps, const Turn& u, const LaneMap& m, int half,
+                                         float* swap) {
   float2 a[2] = {{r.a[0], r.a[1]}, {r.a[2], r.a[3]}}, b[2] = {{r.b[0], r.b[1]}, {r.b[2], r.b[3]}};
   if (norm) {
     float2 s2 = __fmul2_rn(a[0], a[0]);
@@ -237,6 +271,27 @@ __device__ __forceinline__ void turn_row(HeadRow& r, bool norm, float eps, const
       a[i] = __fmul2_rn(a[i], f2);
       b[i] = __fmul2_rn(b[i], f2);
     }
+  }
+  if constexpr (kSwap) {
+    const float v[2][4] = {{a[0].x, a[0].y, a[1].x, a[1].y}, {b[0].x, b[0].y, b[1].x, b[1].y}};
+    const float c[2][4] = {{u.ca[0].x, u.ca[0].y, u.ca[1].x, u.ca[1].y}, {u.cb[0].x, u.cb[0].y, u.cb[1].x, u.cb[1].y}};
+    const float z[2][4] = {{u.sa[0].x, u.sa[0].y, u.sa[1].x, u.sa[1].y}, {u.sb[0].x, u.sb[0].y, u.sb[1].x, u.sb[1].y}};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) swap[swap_at(k ? m.cb[i] : m.ca[i])] = v[k][i];
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ch = k ? m.cb[i] : m.ca[i];
+        float x = v[k][i] * c[k][i];
+        if (u.on & (1u << (4 * k + i))) x = fmaf(swap[swap_at(ch < half ? ch + half : ch - half)], z[k][i], x);
+        if (k) r.b[i] = x;
+        else r.a[i] = x;
+      }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -286,7 +341,7 @@ __device__ __forceinline__ uint32_t length_of(const RaggedLengthsT<N>& p, int b)
   return p.tokens[b];
 }
 
-template <class T, bool kHalf, bool kWide, class Plan>
+template <class T, bool kHalf, bool kWide, bool kSwap, class Plan>
 __global__ void __launch_bounds__(kThreads, heads_ctas(sizeof(T), kWide)) heads_kernel(const HeadsArgs a, const __grid_constant__ Plan plan) {
   __shared__ float2 table[kTokTile][64];
   const int tiles = is_append<Plan> ? 1 : (a.tokens + a.tile - 1) / a.tile;
@@ -315,7 +370,10 @@ __global__ void __launch_bounds__(kThreads, heads_ctas(sizeof(T), kWide)) heads_
     }
   }
   const int l = threadIdx.x & 15;
-  const LaneMap m = lane_map<kHalf, kWide>(rot, l);
+  const LaneMap m = lane_map<kHalf, kWide, kSwap>(rot, l);
+  // two swap rows per half-warp in turn: one barrier per row is enough
+  __shared__ float swap_rows[kSwap ? kRowSlots : 1][2][kSwap ? kSwapRow : 1];
+  int swap_row = 0;
   __syncthreads();
   // half-warp `slot` takes one token of the tile and every `step`-th head, so its token's
   // cosines, sines and the weights stay in registers
@@ -337,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, heads_ctas(sizeof(T), kWide)) heads_
         w.b[i] = x.weight[m.cb[i]];
       }
     }
-    const Turn u = lane_turn<kHalf, kWide>(table[t], w, m, which < 2 ? rot : 0);
+    const Turn u = lane_turn<kHalf, kWide, kSwap>(table[t], w, norm ? x.weight : nullptr, m, which < 2 ? rot : 0);
     const T* src = reinterpret_cast<const T*>(x.data) + b * x.batch_stride + (t0 + t) * x.token_stride;
     uint16_t* dst = x.out;
     size_t pitch;  // between heads of the output
@@ -369,7 +427,10 @@ __global__ void __launch_bounds__(kThreads, heads_ctas(sizeof(T), kWide)) heads_
         if (d > 0 && hb + d * step >= x.heads) break;  // CTA-uniform
         HeadRow y = in[d].get();
         if (left > 0) in[d].issue(src, m);
-        if (which < 2) turn_row<kHalf, kWide>(y, norm, a.eps, u);
+        if (which < 2) {
+          turn_row<kHalf, kWide, kSwap>(y, norm, a.eps, u, m, rot / 2, swap_rows[kSwap ? slot : 0][swap_row]);
+          if (kSwap) swap_row ^= 1;
+        }
         if (mine && left > -kDepth * step) store_row<kHalf, kWide>(dst, y, m);
         left -= step;
         src += src_step;
@@ -379,17 +440,16 @@ __global__ void __launch_bounds__(kThreads, heads_ctas(sizeof(T), kWide)) heads_
   }
 }
 
-template <class T, bool kHalf, bool kWide, class Plan>
+template <class T, bool kHalf, bool kWide, bool kSwap, class Plan>
 cudaError_t launch_heads_t(const HeadsArgs& a, const Plan& plan, cudaStream_t stream) {
   const long tiles = is_append<Plan> ? 1 : (a.tokens + (long)a.tile - 1) / a.tile;
-  heads_kernel<T, kHalf, kWide, Plan><<<(unsigned)(tiles * a.batch), kThreads, 0, stream>>>(a, plan);
+  heads_kernel<T, kHalf, kWide, kSwap, Plan><<<(unsigned)(tiles * a.batch), kThreads, 0, stream>>>(a, plan);
   return cudaGetLastError();
 }
 
 // Vector accesses need four consecutive elements aligned to their size everywhere.
 bool wide_ok(const HeadsArgs& a) {
   const int bytes = a.dtype == PACKKV_DTYPE_FP32 ? 16 : 8;
-  if (a.rope.layout == PACKKV_ROPE_HALF && a.rope.rot_dim % 8 != 0) return false;
   for (const HeadsTensor& x : a.x) {
     if (x.data == nullptr) continue;
     if (reinterpret_cast<uintptr_t>(x.data) % bytes != 0) return false;
@@ -401,11 +461,12 @@ bool wide_ok(const HeadsArgs& a) {
 template <class T, class Plan>
 cudaError_t launch_heads_d(const HeadsArgs& a, const Plan& plan, cudaStream_t stream) {
   const bool half = a.rope.layout == PACKKV_ROPE_HALF;
-  if (wide_ok(a))
-    return half ? launch_heads_t<T, true, true, Plan>(a, plan, stream)
-                : launch_heads_t<T, false, true, Plan>(a, plan, stream);
-  return half ? launch_heads_t<T, true, false, Plan>(a, plan, stream)
-              : launch_heads_t<T, false, false, Plan>(a, plan, stream);
+  if (!wide_ok(a))
+    return half ? launch_heads_t<T, true, false, false, Plan>(a, plan, stream)
+                : launch_heads_t<T, false, false, false, Plan>(a, plan, stream);
+  if (!half) return launch_heads_t<T, false, true, false, Plan>(a, plan, stream);
+  return a.rope.rot_dim % 8 == 0 ? launch_heads_t<T, true, true, false, Plan>(a, plan, stream)
+                                 : launch_heads_t<T, true, true, true, Plan>(a, plan, stream);
 }
 
 template <class Plan>
