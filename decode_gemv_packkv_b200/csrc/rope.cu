@@ -32,8 +32,9 @@ constexpr int kThreads = 128;
 constexpr int kRowSlots = kThreads / 16;     // heads side by side in a CTA
 constexpr int kTokTile = kRowSlots;          // most tokens of a CTA: one per half-warp
 constexpr int kDepth = 4;                    // rows a half-warp has in flight
-// Resident CTAs per SM that the registers are sized for.
-constexpr int heads_ctas(int size, bool wide) { return !wide ? 1 : (size == 2 ? 6 : 4); }
+// Resident CTAs per SM that the registers are sized for (4 x 4096 tokens; 16-bit rows: six 70,
+// eight 75, five 77 us; swapping ones: five 85, six 89; fp32 rows: five 116, four 129, six 124).
+constexpr int heads_ctas(int size, bool wide, bool swap) { return !wide ? 1 : (size == 2 && !swap ? 6 : 5); }
 
 template <class T>
 struct Vec4;  // four consecutive elements
@@ -342,7 +343,7 @@ __device__ __forceinline__ uint32_t length_of(const RaggedLengthsT<N>& p, int b)
 }
 
 template <class T, bool kHalf, bool kWide, bool kSwap, class Plan>
-__global__ void __launch_bounds__(kThreads, heads_ctas(sizeof(T), kWide)) heads_kernel(const HeadsArgs a, const __grid_constant__ Plan plan) {
+__global__ void __launch_bounds__(kThreads, heads_ctas(sizeof(T), kWide, kSwap)) heads_kernel(const HeadsArgs a, const __grid_constant__ Plan plan) {
   __shared__ float2 table[kTokTile][64];
   const int tiles = is_append<Plan> ? 1 : (a.tokens + a.tile - 1) / a.tile;
   const int b = blockIdx.x / tiles;

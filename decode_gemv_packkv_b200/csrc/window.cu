@@ -282,6 +282,8 @@ __device__ __forceinline__ void tail_scores32(const uint16_t* tail, const uint16
 // channel 16m + 8x + j: lane (g, t) reads 8 channels of its tokens per half x.  With an
 // infinity or NaN among the values the tokens are added one by one, those of zero weight
 // (masked ones) left out, so that it does not spread.
+// (On the CUDA cores, a token or four channels per lane, 16 x 32 heads over 1024 tokens with
+// a tail of 118 took 39.0 us, this way 29.7.)
 template <int G>
 __device__ __forceinline__ void tail_values32(const uint16_t* tail, const float* sc, int n, float* sacc, int lane) {
   const int g = lane >> 2, t = lane & 3;
@@ -360,66 +362,6 @@ __device__ __forceinline__ void tail_values32(const uint16_t* tail, const float*
   }
   __syncwarp();
 }
-
-// Scores of n <= 32 tail tokens on the CUDA cores: lane = token.
-template <int G>
-__device__ __forceinline__ void tail_scores_lanes(const uint16_t* tail, const uint16_t* q, int n, float scale, float* sc,
-                                                 int lane) {
-  float s[G];
-#pragma unroll
-  for (int hd = 0; hd < G; ++hd) s[hd] = 0.f;
-  const uint4* row = reinterpret_cast<const uint4*>(tail + (size_t)min(lane, n - 1) * 128);
-#pragma unroll 2
-  for (int c = 0; c < 16; ++c) {
-    const uint4 x = row[c];
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int hd = 0; hd < G; ++hd) {
-      const uint4 y = reinterpret_cast<const uint4*>(q + hd * 128)[c];
-      const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&xw[i]));
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&yw[i]));
-        s[hd] = fmaf(u.x, v.x, s[hd]);
-        s[hd] = fmaf(u.y, v.y, s[hd]);
-      }
-    }
-  }
-  if (lane < n) {
-#pragma unroll
-    for (int hd = 0; hd < G; ++hd) sc[hd * 128 + lane] = scale * s[hd];
-  }
-}
-
-// Adds sum_t p[head][t] v[t][c]: lane = channels 4*lane + i.  Tokens of zero weight (masked
-// ones) are left out, so an infinity or NaN there does not spread.
-template <int G>
-__device__ __forceinline__ void tail_values_lanes(const uint16_t* tail, const float* sc, int n, float* sacc, int lane) {
-  float4 s[G];
-#pragma unroll
-  for (int hd = 0; hd < G; ++hd) s[hd] = reinterpret_cast<const float4*>(sacc + hd * 128)[lane];
-#pragma unroll 4
-  for (int t = 0; t < n; ++t) {
-    const uint2 x = reinterpret_cast<const uint2*>(tail + (size_t)t * 128)[lane];
-    const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
-#pragma unroll
-    for (int hd = 0; hd < G; ++hd) {
-      const float p = sc[hd * 128 + t];
-      if (p != 0.f) {
-        s[hd].x = fmaf(p, u.x, s[hd].x);
-        s[hd].y = fmaf(p, u.y, s[hd].y);
-        s[hd].z = fmaf(p, v.x, s[hd].z);
-        s[hd].w = fmaf(p, v.y, s[hd].w);
-      }
-    }
-  }
-#pragma unroll
-  for (int hd = 0; hd < G; ++hd) reinterpret_cast<float4*>(sacc + hd * 128)[lane] = s[hd];
-  __syncwarp();
-}
-
 
 // ---- the kernel --------------------------------------------------------------------
 // A warp takes an item at a time.  Two ways to share the items out:
@@ -634,8 +576,7 @@ __global__ void __launch_bounds__(kWinWarps * 32, win_ctas(BITS, G, kEven))
     }
     bool ok = true;
     if (tail) {
-      if constexpr (kEven && G <= 2) tail_scores_lanes<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
-      else tail_scores32<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
+      tail_scores32<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
     } else if (kind_k == kKindInvalid) {
       ok = false;
     } else {
@@ -707,8 +648,7 @@ __global__ void __launch_bounds__(kWinWarps * 32, win_ctas(BITS, G, kEven))
       for (int hd = 0; hd < G; ++hd)
         *reinterpret_cast<float4*>(sc + hd * 128 + 4 * lane) = make_float4(pr[hd][0], pr[hd][1], pr[hd][2], pr[hd][3]);
       __syncwarp();
-      if constexpr (kEven && G <= 2) tail_values_lanes<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
-      else tail_values32<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
+      tail_values32<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
     } else if (kind_v == kKindInvalid) {
       ok = false;
     } else if (ok) {
@@ -978,7 +918,8 @@ cudaError_t clusters(WindowArgs a, const Plan& plan, int g, const WinKernel& k, 
 //   2 x 32 kv heads x 4 rows, 18 blocks:  E2 15.1 E4 15.5 C2 16.1  C4 16.8 (35 30 52 42)
 //   16 x 8 kv heads x 4 rows, 33 blocks:  E2 28.7 E4 29.7 C4 32.7  E1 40.6 (124 87 102 210)
 // so: single rows while they give every scheduler of the device at most one item, pairs
-// while they fill at most half of the warps it holds, both in clusters; else four rows.
+// while they fill at most half of the warps it holds, both in clusters; else four rows (or
+// what there is), in clusters while those items fill at most half of the warps.
 template <class Plan>
 cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
   long per_head = 0;  // items of one kv head over all sequences

@@ -170,6 +170,27 @@ def test_masked_infinities_do_not_spread(pk):
     assert torch.all(torch.isnan(out[0, 7]))     # a NaN key that it sees
 
 
+def test_masked_infinities_in_the_even_split(pk):
+    """The same with enough sequences that every warp takes several items: the last tail token
+    is infinite in half of them and seen by the last of two queries alone."""
+    B, H = 96, 16
+    k, v, _ = synth.small_case(3, 1, H, 1, 300)
+    cache = pk.PackKVCache(B, H, 2, 4, ragged=True, keep_perm=True)
+    kd, vd = to_dev(k).expand(B, -1, -1, -1), to_dev(v).expand(B, -1, -1, -1)
+    pk.packkv_encode_block(cache, kd[:, :, :256].contiguous(), vd[:, :, :256].contiguous(), 2)
+    cache.k_tail[:, :, :44] = kd[:, :, 256:]
+    cache.v_tail[:, :, :44] = vd[:, :, 256:]
+    cache.set_lengths([2] * B, [44] * B)
+    q = to_dev(_queries(B, H * 2, 5))
+    clean, out = torch.empty((B, H * 2, 128), device="cuda"), torch.empty((B, H * 2, 128), device="cuda")
+    pk.packkv_attention_window(cache, q, SCALE, clean, 1000, queries=2)
+    cache.v_tail[::2, :, 43, 17] = float("-inf")
+    pk.packkv_attention_window(cache, q, SCALE, out, 1000, queries=2)
+    assert torch.all(torch.isclose(out[:, 0::2], clean[:, 0::2], rtol=1e-5, atol=1e-6))
+    assert torch.equal(out[1::2], clean[1::2])
+    assert torch.all(torch.isinf(out[::2, 1::2, 17])) and torch.all(torch.isfinite(out[::2, 1::2, 18:]))
+
+
 def test_nan_and_infinite_queries(pk):
     cache, _ = _caches(pk, 1, 1, 3, [300], 4)
     q = torch.randn(1, 2, 128, device="cuda").half()
