@@ -216,11 +216,11 @@ class PackKVCache:
 
     @property
     def seq_blocks(self):
-        return list(self._seq_blocks) if self.ragged else [self.s.n_blocks] * self.batch
+        return self._seq_blocks[:] if self.ragged else [self.s.n_blocks] * self.batch
 
     @property
     def seq_tail(self):
-        return list(self._seq_tail) if self.ragged else [self.s.tail_len] * self.batch
+        return self._seq_tail[:] if self.ragged else [self.s.tail_len] * self.batch
 
     def set_lengths(self, blocks, tail=0):
         """Sets the host counters: packed blocks and tail tokens of the cache (ints), or of
