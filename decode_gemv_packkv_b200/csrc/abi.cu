@@ -656,12 +656,16 @@ packkv_status packkv_attention_window(const packkv_cache* cache, const uint16_t*
   a.scale = scale;
   a.out = out;
   a.partials = reinterpret_cast<float*>(ws);
-  if (!is_ragged(cache)) return cuda_status(packkv::launch_window(a, nullptr, as_stream(stream)));
+  if (!is_ragged(cache)) {
+    if (!packkv::window_countable(a, nullptr)) return PACKKV_ERR_UNSUPPORTED;
+    return cuda_status(packkv::launch_window(a, nullptr, as_stream(stream)));
+  }
   WindowPlan& plan = plan_of<WindowPlan>();
   for (int b = 0; b < cache->batch; ++b) {
     plan.blocks[b] = cache->seq_blocks[b];
     plan.tail[b] = (uint8_t)cache->seq_tail[b];
   }
+  if (!packkv::window_countable(a, &plan)) return PACKKV_ERR_UNSUPPORTED;
   return cuda_status(packkv::launch_window(a, &plan, as_stream(stream)));
 }
 

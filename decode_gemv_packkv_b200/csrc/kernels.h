@@ -206,6 +206,8 @@ struct WindowPlanT {  // ragged batches: what every sequence holds, and its rows
 };
 using WindowPlan = WindowPlanT<kMaxRaggedBatch>;
 size_t window_workspace_bytes(int batch, int kv_heads, int rows);
+// Whether the items of all rows can be counted in 31 bits.
+bool window_countable(const WindowArgs& a, const WindowPlan* plan);
 // plan: blocks and tail of every sequence filled in (ragged batches), or NULL
 cudaError_t launch_window(WindowArgs a, const WindowPlan* plan, cudaStream_t stream);
 

@@ -76,7 +76,7 @@ __device__ __forceinline__ float4 param4(const unsigned char* st, int at, int la
 template <class Plan>
 constexpr bool kRagged = !std::is_same<Plan, NoPlan>::value;
 
-// A place in the list of all items: (sequence, kv head, chunk of 8 query rows), item.
+// A place in the list of all items: (sequence, kv head, chunk of query rows), item.
 struct ItemCursor {
   int b, h, chunk, i;
   ItemList items;  // of the sequence
@@ -148,8 +148,8 @@ __device__ __forceinline__ long entry_of(const WindowArgs& a, int b, int h, int 
 template <int BITS>
 __device__ __forceinline__ int entry_kind(const WindowArgs& a, uint2 e) {
   constexpr uint32_t raw = (uint32_t)raw_record_bytes(BITS);
-  const bool valid = e.x != 0xFFFFFFFFu && e.y >= 1040 / 16 && e.y * 16u <= raw && (uint64_t)e.x + e.y <= a.arena16;
-  return !valid ? kKindInvalid : (e.y * 16u == raw ? kKindRaw : kKindPacked);
+  const bool valid = e.x != 0xFFFFFFFFu && e.y >= 1040 / 16 && e.y <= raw / 16 && (uint64_t)e.x + e.y <= a.arena16;
+  return !valid ? kKindInvalid : (e.y == raw / 16 ? kKindRaw : kKindPacked);
 }
 
 // What a query row sees of the 128 (or fewer) tokens from pos0 on, as bounds on the offset
@@ -240,9 +240,9 @@ __device__ __forceinline__ void hmma16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Scaled scores of n <= 32 tail tokens into sc[head*128 + t].  The contraction's channel order is free: lane (g, t) takes
-// channels 32 kk + 8t .. +7 of its token (A) and of its head (B) with one 16-byte load
-// each, two k-steps per load.  Exact products, fp32 sums.
+// Scaled scores of n <= 32 tail tokens into sc[head*128 + t].  The contraction's channel
+// order is free: lane (g, t) takes channels 32 kk + 8t .. +7 of its token (A) and of its
+// head (B) with one 16-byte load each, two k-steps per load.  Exact products, fp32 sums.
 template <int G>
 __device__ __forceinline__ void tail_scores32(const uint16_t* tail, const uint16_t* q, int n, float scale, float* sc,
                                               int lane) {
@@ -907,6 +907,24 @@ cudaError_t clusters(WindowArgs a, const Plan& plan, int g, const WinKernel& k, 
   return cudaLaunchKernelExC(&cfg, k.fn, args);
 }
 
+// Items of one kv head over all sequences, and of the longest row.
+template <class Plan>
+long items_per_head(const WindowArgs& a, const Plan* plan, int* most) {
+  if constexpr (kRagged<Plan>) {
+    long sum = 0;
+    *most = 0;
+    for (int b = 0; b < a.batch; ++b) {
+      const int n = item_list(a.queries, a.window, a.sinks, plan->blocks[b], plan->tail[b]).n;
+      if (n > *most) *most = n;
+      sum += n;
+    }
+    return sum;
+  } else {
+    *most = item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len).n;
+    return (long)a.batch * *most;
+  }
+}
+
 // Query rows of a chunk (1, 2 or 4) and the form.  A record's codes are read and masked
 // once per chunk, so larger chunks do less work in all; smaller ones spread it over more
 // warps.  Measured (us, E the even split, C clusters, digits the chunk's rows; uncompressed
@@ -922,17 +940,7 @@ cudaError_t clusters(WindowArgs a, const Plan& plan, int g, const WinKernel& k, 
 // what there is), in clusters while those items fill at most half of the warps.
 template <class Plan>
 cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
-  long per_head = 0;  // items of one kv head over all sequences
-  if constexpr (kRagged<Plan>) {
-    for (int b = 0; b < a.batch; ++b) {
-      const int n = item_list(a.queries, a.window, a.sinks, plan.blocks[b], plan.tail[b]).n;
-      if (n > a.most_items) a.most_items = n;
-      per_head += n;
-    }
-  } else {
-    a.most_items = item_list(a.queries, a.window, a.sinks, a.n_blocks, a.tail_len).n;
-    per_head = (long)a.batch * a.most_items;
-  }
+  const long per_head = items_per_head(a, &plan, &a.most_items);
   auto items = [&](int g) { return per_head * a.kv_heads * (a.rows / g); };
   int sms = 0, dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -956,7 +964,6 @@ cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cluster = cluster || 2 * items(g) <= (long)ctas * kWinWarps;
   a.n_items = items(g);
-  if (a.n_items > 0x7fffffffL) return cudaErrorInvalidValue;
   if constexpr (kRagged<Plan>) {
     long at = 0;
     for (int b = 0; b < a.batch; ++b) {
@@ -973,6 +980,13 @@ cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
 }
 
 }  // namespace
+
+bool window_countable(const WindowArgs& a, const WindowPlan* plan) {
+  int most = 0;
+  const NoPlan none;
+  const long per_head = plan ? items_per_head(a, plan, &most) : items_per_head(a, &none, &most);
+  return per_head <= 0x7fffffffL / ((long)a.kv_heads * a.rows);
+}
 
 size_t window_workspace_bytes(int batch, int kv_heads, int rows) {
   // (parts + (row, chunk)s) slots of a chunk's rows: at most this for any chunk

@@ -380,8 +380,10 @@ packkv_status packkv_append_norm_rope(packkv_cache* cache, const packkv_rope* ro
  * so a block that is seen in part is masked through cache->perm, which must be set
  * unless reorder_key is PACKKV_KEY_IDENTITY (PACKKV_ERR_INVALID_ARG).  A seen block with
  * an invalid or freed index entry sets PACKKV_DEV_BAD_RECORD and its tokens are left
- * out.  ws as for packkv_attention_decode (packkv_attention_window_workspace_bytes); results
- * do not depend on the launch's timing.
+ * out.  More than 2^31 - 1 seen (block, query row) pairs in one call are
+ * PACKKV_ERR_UNSUPPORTED.  ws as for packkv_attention_decode
+ * (packkv_attention_window_workspace_bytes); results do not depend on the launch's
+ * timing.
  */
 size_t packkv_attention_window_workspace_bytes(const packkv_cache* cache, int32_t q_heads);
 packkv_status packkv_attention_window(const packkv_cache* cache, const uint16_t* q, int32_t q_heads,

@@ -113,6 +113,9 @@ def test_window_refusals(pk):
     assert run(s) == bad
     s.perm = None
     assert run(s) == bad                                           # reordered, no permutations
+    big = _fake_cache(pk, batch=1 << 14, kv_heads=1 << 10, max_blocks=2000, n_blocks=2000)
+    big.perm = 0x11000000
+    assert run(big, q_heads=64 << 10, window=1 << 30) == pk.ERR_UNSUPPORTED  # 2^41 items
 
 
 def test_block_call_refusals(pk):
