@@ -470,6 +470,8 @@ def packkv_norm_rope(rope: Rope | None, q, k, v, q_out=None, k_out=None, v_out=N
                 or not positions.is_contiguous()):
             raise ValueError(f"positions must be a contiguous int32 {(B, T)} on the inputs' device")
         pos = positions.data_ptr()
+    if B == 0 or T == 0:  # nothing to do (and such tensors have no address)
+        return
     status = _lib.packkv_norm_rope(None if rope is None else rope.ref, heads, B, T, pos, first, *ptrs,
                                    _stream_of(like, stream))
     if status:

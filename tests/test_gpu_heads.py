@@ -276,3 +276,14 @@ def test_refusals(pk):
     assert e.value.status == pk.ERR_UNSUPPORTED
     with pytest.raises(ValueError):
         pk.packkv_append_norm_rope(cache, None, None, x[:, 0], x[:, 0])
+
+
+@pytest.mark.parametrize("shape", [(2, 0), (0, 3)])
+def test_no_tokens(pk, shape):
+    """Tensors without elements have no address; a call on them does nothing."""
+    B, T = shape
+    x = torch.empty((B, T, 3, 128), dtype=torch.float16, device="cuda")
+    out = torch.empty((B, 3, T, 128), dtype=torch.float16, device="cuda")
+    pk.packkv_norm_rope(pk.Rope(), x, x, x, out, out, out, eps=1e-6)
+    with pytest.raises(ValueError):
+        pk.packkv_norm_rope(None, x, None, None, q_out=out.float())

@@ -289,3 +289,60 @@ def test_refusals_of_the_binding(pk):
     with pytest.raises(pk.PackKVError) as e:
         pk.packkv_attention_window(cache, q, 1.0, out, 8, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == pk.ERR_INVALID_ARG
+
+
+def test_uniform_batch_beyond_the_ragged_limit(pk):
+    """More sequences than a ragged cache may have; everything in the window."""
+    B, T = 2100, 150
+    k, v = (torch.randn(B, 1, T, 128, generator=torch.Generator().manual_seed(s)).half().cuda() for s in (1, 2))
+    cache = pk.PackKVCache(B, 1, 2, 3, keep_perm=True)
+    pk.prefill(cache, k, v)
+    q = to_dev(_queries(B, 4, 11))
+    out, full = torch.empty(q.shape, device="cuda"), torch.empty(q.shape, device="cuda")
+    pk.packkv_attention_window(cache, q, SCALE, out, T)
+    pk.packkv_attention_decode(cache, q, SCALE, full)
+    assert torch.linalg.norm(out - full) <= 2e-5 * torch.linalg.norm(full)
+    assert pk.packkv_get_status(cache) == 0
+
+
+def test_two_calls_at_once(pk):
+    """Two streams, a workspace each, over one cache: the bits of calls made one by one."""
+    cache, _ = _caches(pk, 4, 8, 4, [2000, 1000, 500, 90], 9)
+    qs = [to_dev(_queries(4, 32, s)) for s in (1, 2)]
+    outs = [torch.empty((4, 32, 128), device="cuda") for _ in qs]
+    want = []
+    for q, out in zip(qs, outs):
+        pk.packkv_attention_window(cache, q, SCALE, out, 1500)
+        want.append(out.clone())
+    need = cache.window_workspace(32).nbytes
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, out, w, stream in zip(qs, outs, ws, streams):
+            pk.packkv_attention_window(cache, q, SCALE, out, 1500, ws=w, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+def test_records_past_four_gib(pk, bits):
+    """Records whose offsets in bytes pass 32 bits: the window reads them where they are, and
+    compaction brings them to the start of a small cache."""
+    tokens, at = 700, 5 << 30
+    k, v, _ = synth.small_case(19, 2, 2, 1, tokens)
+    caches = [pk.PackKVCache(2, 2, 5, bits, keep_perm=True),
+              pk.PackKVCache(2, 2, 5, bits, keep_perm=True, arena_bytes=at + (1 << 20)),
+              pk.PackKVCache(2, 2, 5, bits, keep_perm=True)]
+    low, high, back = caches
+    high.ctrl[:2] = at // 16
+    q = to_dev(_queries(2, 8, 4))
+    for cache in (low, high):
+        pk.prefill(cache, to_dev(k), to_dev(v))
+    pk.packkv_compact(back, high)
+    outs = [torch.empty((2, 8, 128), device="cuda") for _ in caches]
+    for cache, out in zip(caches, outs):
+        pk.packkv_attention_window(cache, q, SCALE, out, 600, sinks=4)
+        assert pk.packkv_get_status(cache) == 0
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    assert int(high.k_index[..., 0].long().bitwise_and(0xFFFFFFFF).min()) >= at // 16
