@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(kWinWarps * 32, win_ctas(BITS, G, kEven))
     bool ok = true;
     if (tail) {
       tail_scores32<G>(a.k_tail + tail_at, qrow, n_tok, a.scale, sc, lane);
-    } else if (kind_k == kKindInvalid) {
-      ok = false;
+    } else if (kind_k == kKindInvalid || kind_v == kKindInvalid) {
+      ok = false;  // before the softmax: neither the sums nor the maximum know the block
     } else {
       ok = record_scores<BITS, G>(m.stage(0), kind_k | (len_k << 8), m.table(), qr, sc, a.scale, lane);
     }
@@ -649,8 +649,6 @@ __global__ void __launch_bounds__(kWinWarps * 32, win_ctas(BITS, G, kEven))
         *reinterpret_cast<float4*>(sc + hd * 128 + 4 * lane) = make_float4(pr[hd][0], pr[hd][1], pr[hd][2], pr[hd][3]);
       __syncwarp();
       tail_values32<G>(a.v_tail + tail_at, sc, n_tok, sacc, lane);
-    } else if (kind_v == kKindInvalid) {
-      ok = false;
     } else if (ok) {
       ok = record_values<BITS, G>(m.stage(1), kind_v | (len_v << 8), m.table(), pr, acc_lo, acc_hi, sacc, mp, lane);
     }

@@ -378,10 +378,12 @@ packkv_status packkv_append_norm_rope(packkv_cache* cache, const packkv_rope* ro
  * window >= 1 (window >= T_b: all tokens up to p), sinks >= 0.  Blocks that no query
  * sees are not read: they may have been freed.  The tokens inside a block are reordered,
  * so a block that is seen in part is masked through cache->perm, which must be set
- * unless reorder_key is PACKKV_KEY_IDENTITY (PACKKV_ERR_INVALID_ARG).  A seen block with
- * an invalid or freed index entry sets PACKKV_DEV_BAD_RECORD and its tokens are left
- * out.  More than 2^31 - 1 seen (block, query row) pairs in one call are
- * PACKKV_ERR_UNSUPPORTED.  ws as for packkv_attention_decode
+ * unless reorder_key is PACKKV_KEY_IDENTITY (PACKKV_ERR_INVALID_ARG).  A seen block whose
+ * K or V index entry is invalid or freed sets PACKKV_DEV_BAD_RECORD and its tokens are
+ * left out of the softmax.  A compressed record whose contents do not fit its length sets
+ * the bit too; in K its tokens are left out, in V (read behind the softmax) the outputs of
+ * the rows that see it are unspecified.  More than 2^31 - 1 seen (block, query row) pairs
+ * in one call are PACKKV_ERR_UNSUPPORTED.  ws as for packkv_attention_decode
  * (packkv_attention_window_workspace_bytes); results do not depend on the launch's
  * timing.
  */
