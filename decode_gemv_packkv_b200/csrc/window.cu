@@ -178,6 +178,13 @@ __device__ __forceinline__ WholeBlocks whole_blocks(const WindowArgs& a, const I
   return w;
 }
 
+// Two fp16 of a query, infinities made NaN: the digits cannot carry an infinity, and scores
+// of -inf alone would look like a row that sees nothing; a NaN reaches every score (through
+// the records' min term, through the tail's products).
+__device__ __forceinline__ uint32_t inf_to_nan(uint32_t w) {
+  return w | ((((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u) >> 6);  // exponent all ones: the top mantissa bit
+}
+
 // Scores of a staged K record into sc; false: the record failed its checks.
 template <int BITS, int G>
 __device__ __forceinline__ bool record_scores(unsigned char* st, int kind_len, uint32_t* tab, const float (&qr)[G][4],
@@ -250,8 +257,10 @@ __device__ __forceinline__ void tail_scores32(const uint16_t* tail, const uint16
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   uint4 qb[4];
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk)
+  for (int kk = 0; kk < 4; ++kk) {
     qb[kk] = g < G ? *reinterpret_cast<const uint4*>(q + (size_t)g * 128 + 32 * kk + 8 * t) : zero;
+    qb[kk] = make_uint4(inf_to_nan(qb[kk].x), inf_to_nan(qb[kk].y), inf_to_nan(qb[kk].z), inf_to_nan(qb[kk].w));
+  }
 #pragma unroll
   for (int tile = 0; tile < 2; ++tile) {
     if (16 * tile >= n) break;
@@ -540,7 +549,9 @@ __global__ void __launch_bounds__(kWinWarps * 32, win_ctas(BITS, G, kEven))
       whole_of = whole_blocks(a, cc.items);
 #pragma unroll
       for (int hd = 0; hd < G; ++hd) {
-        const uint2 v = *reinterpret_cast<const uint2*>(qrow + hd * 128 + 4 * lane);
+        uint2 v = *reinterpret_cast<const uint2*>(qrow + hd * 128 + 4 * lane);
+        v.x = inf_to_nan(v.x);
+        v.y = inf_to_nan(v.y);
         const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
         const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
         qr[hd][0] = u.x;

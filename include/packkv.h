@@ -374,7 +374,8 @@ packkv_status packkv_append_norm_rope(packkv_cache* cache, const packkv_rope* ro
  *   q:   device fp16 [batch][q_heads][128]; q_heads = kv_heads * queries * G; row
  *        (h*queries + s)*G + g is query head g of kv head h at position s.
  *        queries * G in {1,2,4,8,16,32,64}.
- *   out: device fp32 [batch][q_heads][128].  A row that sees no token is zero.
+ *   out: device fp32 [batch][q_heads][128].  A row that sees no token (or only tokens of
+ *        score -inf) is zero; a row whose q holds an infinity or NaN and that sees one is NaN.
  * window >= 1 (window >= T_b: all tokens up to p), sinks >= 0.  Blocks that no query
  * sees are not read: they may have been freed.  The tokens inside a block are reordered,
  * so a block that is seen in part is masked through cache->perm, which must be set
