@@ -334,6 +334,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, attn_min_ctas(BITS, G))
       if (x + 1 - wk.base >= 32) wk.load(ka, plan, x + 1, hi, lane);
       issue_item<BITS, G, false>(ka, m, nc, wk.get(x + 1), 0, lane);
     }
+    // the V record is issued, so its kind is known: a block without one is left out before
+    // the softmax, not by its values alone
+    skip |= (*m.kind(1) & 0xFF) == kKindInvalid;
 
     // ---- online softmax: running max and sum of exp per head, p of this lane's slots
     float pr[G][4];

@@ -267,8 +267,9 @@ packkv_status packkv_pv_gemv_noalloc(const packkv_cache* cache, const float* p, 
  *   ws:  device, ws_bytes >= packkv_attention_workspace_bytes(cache, q_heads)
  *        (no initialisation needed; two calls sharing ws must not overlap in time).
  * T == 0 (nothing to attend to) is PACKKV_ERR_INVALID_ARG for a uniform batch; in a
- * ragged batch a sequence without tokens gets zero outputs.  A record with an
- * invalid index entry sets PACKKV_DEV_BAD_RECORD and its tokens are left out.
+ * ragged batch a sequence without tokens gets zero outputs.  A block whose K or V
+ * index entry is invalid sets PACKKV_DEV_BAD_RECORD and its tokens are left out of the
+ * softmax.
  */
 size_t packkv_attention_workspace_bytes(const packkv_cache* cache, int32_t q_heads);
 packkv_status packkv_attention_decode(const packkv_cache* cache, const uint16_t* q, int32_t q_heads,
