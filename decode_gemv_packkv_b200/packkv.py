@@ -11,6 +11,7 @@ the `packkv_cache` struct that points into them.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import os
 import struct
@@ -256,35 +257,43 @@ class PackKVCache:
     def kv_heads(self) -> int:
         return self.s.kv_heads
 
-    def workspace(self, q_heads: int) -> torch.Tensor:
-        """p·V workspace for q_heads (allocated once, reused by every call)."""
-        if q_heads not in self._ws:
-            n = packkv_workspace_bytes(self, q_heads)
-            self._ws[q_heads] = torch.zeros(max(n, 16), dtype=torch.uint8, device=self.k_arena.device)
-        return self._ws[q_heads]
+    def _workspace(self, key, nbytes, stream):
+        """The cache's workspace `key` (a tuple) on a stream (None: the current one), allocated
+        at its first use.  No call needs it initialised.  Every stream has its own, allocated
+        on that stream: calls on one stream take their turns, so they share it, and no other
+        stream's work (that of an earlier user of the memory among it) can still write to it."""
+        dev = self.k_arena.device
+        if stream is None:
+            handle = torch._C._cuda_getCurrentRawStream(dev.index) if dev.type == "cuda" else 0
+        else:
+            handle = stream.cuda_stream
+        key += (handle,)
+        ws = self._ws.get(key)
+        if ws is None:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                ws = torch.empty(max(nbytes(), 16), dtype=torch.uint8, device=dev)
+            self._ws[key] = ws
+        return ws
 
-    def attention_workspace(self, q_heads: int) -> torch.Tensor:
-        """Fused-attention workspace for q_heads (allocated once, reused by every call)."""
-        key = ("attn", q_heads)
-        if key not in self._ws:
-            n = int(_lib.packkv_attention_workspace_bytes(ctypes.byref(self.s), q_heads))
-            self._ws[key] = torch.zeros(max(n, 16), dtype=torch.uint8, device=self.k_arena.device)
-        return self._ws[key]
+    def workspace(self, q_heads: int, stream=None) -> torch.Tensor:
+        """p·V workspace for q_heads: one per stream (None: the current one), allocated once and
+        reused by every call there.  Graphs captured on one stream share it: replays that
+        overlap in time need workspaces of their own (the calls' ws)."""
+        return self._workspace(("pv", q_heads), lambda: packkv_workspace_bytes(self, q_heads), stream)
 
-    def window_workspace(self, q_heads: int) -> torch.Tensor:
-        """Window-attention workspace for q_heads (allocated once, reused by every call)."""
-        key = ("window", q_heads)
-        if key not in self._ws:
-            n = int(_lib.packkv_attention_window_workspace_bytes(ctypes.byref(self.s), q_heads))
-            self._ws[key] = torch.zeros(max(n, 16), dtype=torch.uint8, device=self.k_arena.device)
-        return self._ws[key]
+    def attention_workspace(self, q_heads: int, stream=None) -> torch.Tensor:
+        """Fused-attention workspace for q_heads (one per stream, as workspace())."""
+        return self._workspace(("attn", q_heads), lambda: int(
+            _lib.packkv_attention_workspace_bytes(ctypes.byref(self.s), q_heads)), stream)
 
-    def compact_workspace(self) -> torch.Tensor:
-        """Workspace of packkv_compact from this cache (allocated once, reused by every call)."""
-        if "compact" not in self._ws:
-            n = packkv_compact_workspace_bytes(self)
-            self._ws["compact"] = torch.empty(max(n, 16), dtype=torch.uint8, device=self.k_arena.device)
-        return self._ws["compact"]
+    def window_workspace(self, q_heads: int, stream=None) -> torch.Tensor:
+        """Window-attention workspace for q_heads (one per stream, as workspace())."""
+        return self._workspace(("window", q_heads), lambda: int(
+            _lib.packkv_attention_window_workspace_bytes(ctypes.byref(self.s), q_heads)), stream)
+
+    def compact_workspace(self, stream=None) -> torch.Tensor:
+        """Workspace of packkv_compact from this cache (one per stream, as workspace())."""
+        return self._workspace(("compact",), lambda: packkv_compact_workspace_bytes(self), stream)
 
     def arena_used(self):
         """(K bytes, V bytes) in use; synchronises."""
@@ -341,7 +350,7 @@ def packkv_pv_gemv(cache: PackKVCache, p: torch.Tensor, out: torch.Tensor, ws: t
     if p.dtype != torch.float32 or p.dim() != 3 or out.dtype != torch.float32:
         raise ValueError("p must be fp32 [B, Hq, ld], out fp32 [B, Hq, 128]")
     if ws is None:
-        ws = cache.workspace(p.shape[1])
+        ws = cache.workspace(p.shape[1], stream)
     _check("packkv_pv_gemv", _lib.packkv_pv_gemv(ctypes.byref(cache.s), _ptr(p), p.shape[2], p.shape[1],
                                                  _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
 
@@ -366,7 +375,7 @@ def packkv_attention_decode(cache: PackKVCache, q: torch.Tensor, scale: float, o
     if q.dtype != torch.float16 or q.dim() != 3 or out.dtype != torch.float32:
         raise ValueError("q must be fp16 [B, Hq, 128], out fp32 [B, Hq, 128]")
     if ws is None:
-        ws = cache.attention_workspace(q.shape[1])
+        ws = cache.attention_workspace(q.shape[1], stream)
     _check("packkv_attention_decode", _lib.packkv_attention_decode(ctypes.byref(cache.s), _ptr(q), q.shape[1],
                                                                    float(scale), _ptr(out), _ptr(ws), ws.numel(),
                                                                    _stream(stream)))
@@ -507,13 +516,16 @@ def packkv_attention_window(cache: PackKVCache, q: torch.Tensor, scale: float, o
     shape, at = q.shape, cache.k_tail.get_device()
     if len(shape) != 3 or shape[0] != cache.s.batch or shape[2] != HEAD_DIM:
         raise ValueError("q must be fp16 [batch, q_heads, 128] on the cache's device")
+    handle = _stream_of(q, stream)
     if ws is None:
-        ws = cache.window_workspace(shape[1])
+        ws = cache._ws.get(("window", shape[1], handle))
+        if ws is None:
+            ws = cache.window_workspace(shape[1], stream)
     # no sequence has more than 2^31 tokens: larger limits mean the same
     window, sinks = min(window, _INT_MAX), min(sinks, _INT_MAX)
     status = _lib.packkv_attention_window(cache.addr, _out_ptr("q", q, torch.float16, shape, at), shape[1], queries,
                                           window, sinks, float(scale), _out_ptr("out", out, torch.float32, shape, at),
-                                          _ws_ptr(ws, at), ws.nbytes, _stream_of(q, stream))
+                                          _ws_ptr(ws, at), ws.nbytes, handle)
     if status:
         _check("packkv_attention_window", status)
 
@@ -555,9 +567,12 @@ def packkv_compact(dst: PackKVCache, src: PackKVCache, ws: torch.Tensor | None =
     at = src.k_arena.get_device()
     if dst.k_arena.get_device() != at:
         raise ValueError("both caches must be on one device")
+    handle = _stream_of(src.k_arena, stream)
     if ws is None:
-        ws = src.compact_workspace()
-    status = _lib.packkv_compact(dst.addr, src.addr, _ws_ptr(ws, at), ws.nbytes, _stream_of(src.k_arena, stream))
+        ws = src._ws.get(("compact", handle))
+        if ws is None:
+            ws = src.compact_workspace(stream)
+    status = _lib.packkv_compact(dst.addr, src.addr, _ws_ptr(ws, at), ws.nbytes, handle)
     if status:
         _check("packkv_compact", status)
 
