@@ -22,6 +22,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "mover.cuh"
 
 namespace packkv {
 
@@ -325,7 +326,6 @@ __global__ void __launch_bounds__(kTile) small_offsets_kernel(const CompactArgs 
 // up side by side and write the new ones, then lane 0 moves the owned records through
 // three shared-memory stages with bulk copies (a load and a store in flight at a time).
 constexpr int kMoveWarps = 4;
-constexpr int kMoveStages = 3;
 constexpr int kBatch = 4;
 
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
@@ -334,49 +334,26 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-struct Mover {  // lane 0's pipeline: load n goes to stage n % 3, store n - 1 is issued after it
-  unsigned char* stage;
+struct BulkPort {  // a warp's stages and their barriers
+  unsigned char* base;
   uint32_t stage_bytes;
   uint64_t* bar;
   uint64_t* ctrl;
-  long n;         // loads issued
-  void* dst;      // of load n - 1, whose store is not issued yet
-  uint32_t bytes;
-  bool dead;      // a load gave up: nothing more is moved
 
-  __device__ void store_last() {
-    if (n == 0 || dead) return;
-    const int s = (int)((n - 1) % kMoveStages);
-    if (!mbar_wait_bounded(bar + s, (uint32_t)(((n - 1) / kMoveStages) & 1), ctrl)) {
-      dead = true;
-      return;
-    }
-    bulk_s2g(dst, stage + s * stage_bytes, bytes);
+  __device__ __forceinline__ void load(int s, const void* from, uint32_t bytes) {
+    mbar_arrive_expect_tx(bar + s, bytes);
+    bulk_g2s(base + s * stage_bytes, from, bytes, bar + s);
   }
-  __device__ void move(void* to, const void* from, uint32_t nbytes) {
-    if (dead) return;
-    const int s = (int)(n % kMoveStages);
-    // stores up to n - 2 are issued; the stage held record n - 3
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    mbar_arrive_expect_tx(bar + s, nbytes);
-    bulk_g2s(stage + s * stage_bytes, from, nbytes, bar + s);
-    store_last();
-    ++n;
-    dst = to;
-    bytes = nbytes;
-  }
-  __device__ void finish() {
-    store_last();
-    if (dead && n > 0) {  // wait, bounded, for the other load in flight
-      const int s = (int)(n % kMoveStages);
-      mbar_wait_bounded(bar + s, (uint32_t)((n / kMoveStages) & 1), ctrl);
-    }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  }
+  __device__ __forceinline__ bool landed(int s, uint32_t phase) { return mbar_wait_bounded(bar + s, phase, ctrl); }
+  __device__ __forceinline__ void store(int s, void* to, uint32_t bytes) { bulk_s2g(to, base + s * stage_bytes, bytes); }
+  __device__ __forceinline__ void await_reads() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+  __device__ __forceinline__ void await_stores() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 };
 
+// Two CTAs per SM, as many as the grid has (registers to spare: at the compiler's own choice of
+// 64 a few were spilled).
 template <int N>
-__global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const CompactArgs a, uint32_t stage_bytes,
+__global__ void __launch_bounds__(kMoveWarps * 32, 2) move_kernel(const CompactArgs a, uint32_t stage_bytes,
                                                               const __grid_constant__ LengthPlanT<N> plan) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t bars[kMoveWarps][kMoveStages];
@@ -398,7 +375,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const CompactArgs
     fence_mbar_init();
   }
   __syncwarp();
-  Mover mv{smem + warp * kMoveStages * stage_bytes, stage_bytes, bars[warp], a.dst.ctrl, 0, nullptr, 0u, false};
+  Mover<BulkPort> mv{{smem + warp * kMoveStages * stage_bytes, stage_bytes, bars[warp], a.dst.ctrl}, 0, nullptr, 0u, false};
   const int64_t batches = (a.entries + kBatch - 1) / kBatch;
   for (int64_t x = warp0; x < batches; x += warps) {
     const int tensor = (lane / kBatch) & 1;
