@@ -81,3 +81,24 @@ def reference(oc, of, q, window, sinks, n_queries, scale=SCALE, without=()):
             out[b, r] = p @ v
             terms[b, r] = p @ np.abs(v)
     return out, terms
+
+
+def whole_softmax_with_digits(oc, q, digits, scale=SCALE):
+    """The oracle's outputs over sequence 0, head 0 (whole blocks, everything seen) with q'
+    rounded as the kernels' integer digits round it: per block q' = q times the channels'
+    steps, scaled to 127 (three digits, 2^-14 the last) or to a power of two below 64 (four,
+    2^-21).  digits None: exact."""
+    k, v = (O.arrival_order(oc, which, 0, 0) for which in "kv")
+    q = np.asarray(q, np.float64)
+    score = scale * q @ k.T
+    for j in range(oc.seq_blocks[0]) if digits else ():
+        block = k[128 * j:128 * j + 128]
+        low = block.min(axis=0)
+        step = (block.max(axis=0) - low) / (2 ** oc.bits - 1)
+        code = (block - low) / np.where(step > 0, step, 1.0)
+        top = np.abs(q * step).max(axis=1, keepdims=True)
+        f = 127 / top if digits == 3 else 2.0 ** (5 - np.floor(np.log2(top)))
+        last = 2.0 ** (14 if digits == 3 else 21)
+        y = np.rint(q * step * f * last) / last
+        score[:, 128 * j:128 * j + 128] = scale * ((y / f) @ code.T + (q @ low)[:, None])
+    return O.softmax(score) @ v
