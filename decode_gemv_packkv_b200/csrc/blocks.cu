@@ -10,12 +10,15 @@
 // complemented entry number, so the order of arrival does not matter) names the first
 // entry of each record.  One pass of a decoupled look-back over tiles of entries sums
 // the lengths of owned records into new offsets; a second kernel copies the records and
-// writes the new entries.  Bound: HBM, 2 bytes moved per live byte.  The 24 k live records of
+// writes the new entries.  Bound: HBM, 2 bytes moved per live byte.  The 22 k live records of
 // 16 x 32 rows of 64 blocks (394 MB moved) take 88 us: 4 marking, 10 summing offsets, 77
-// copying at 5.1 TB/s (a plain copy runs at 6.56); warps that copied with 16-byte loads and
-// stores, four in flight, took 151.
+// copying at 5.1 TB/s (a plain copy runs at 6.56).  The copy is not shared out evenly: a
+// warp's next batch lies 4736 entries on, a multiple of 64, so it stays at the same four block
+// numbers of its rows, and as rows end at different lengths the fullest of the 1184 warps
+// has 44 records, the mean 19 and 52 none (the fullest SM 172, the mean 149).  Warps that
+// copied with 16-byte loads and stores, four in flight, took 151.
 // Forks and frees are a few entries per block: bound by the launch.  Three CTAs per (pair,
-// head), four loads in flight: 32 pairs x 8 heads of 64 blocks in 3.7 us (6.9 with one CTA).
+// head), four loads in flight: 32 pairs x 8 heads of 64 blocks in 3.8 us (6.9 with one CTA).
 #include <atomic>
 
 #include <cuda_runtime.h>

@@ -11,8 +11,8 @@
 // 32 + 8 heads in bf16 (403 MB) takes 69.6 us, 5.8 TB/s; a plain copy runs at 6.56.  What
 // brought it there: a half-warp keeps one token, so that its cosines, sines and weights
 // stay in registers over all heads (93 -> 81 us), four rows in flight, each loaded again as
-// soon as it is converted (-> 75), and registers for six CTAs per SM instead of eight (-> 70:
-// at 64 registers a third of the instructions were the compiler's own moves).
+// soon as it is converted (-> 75), and registers for six CTAs per SM instead of eight (-> 70;
+// 55.7e6 warp instructions at 64 registers, 39.3e6 at 71).
 // A half-warp takes one head at a time; lane l has channels A..A+3 and B..B+3, chosen so
 // that both members of each pair sit in one lane (no shuffles for the rotation): half layout
 // A = 4l, B = rot/2 + 4l (the unrotated rest packed behind), interleaved A = 4l, B = 64 + 4l.
@@ -482,8 +482,9 @@ cudaError_t launch_heads_p(const HeadsArgs& a, const Plan& plan, cudaStream_t st
 cudaError_t launch_prompt_heads(const HeadsArgs& args, cudaStream_t stream) {
   HeadsArgs a = args;
   // A token per half-warp shares its sines and weights between all its heads; fewer tokens
-  // per CTA spread a short prompt over more SMs (3 x 257 tokens of 18 heads: 4.4 us with
-  // four, 8.0 with one; 4 x 4096 of 48: 75 us with eight or sixteen, 88 with four).
+  // per CTA spread a short prompt over more SMs: eight from three CTAs per SM (148 of them)
+  // on, four from one on (3 x 257 tokens of 18 heads: 4.4 us with four, 8.0 with one; 4 x 4096
+  // of 48, at 64 registers: 75 us with eight, 88 with four).
   const long n = (long)a.batch * a.tokens;
   a.tile = n >= 8 * 444 ? 8 : (n >= 4 * 148 ? 4 : 1);
   return launch_heads_p(a, PromptPlan{}, stream);

@@ -11,10 +11,12 @@
 // (decode.cuh), with four digits; the running maximum and sum of the softmax and the value
 // sums are fp32, and neither scores nor probabilities reach global memory.
 //
-// Bound: for many rows the decode's instructions (1690 per warp and 3-bit record pair, 2.15
-// per cycle and SM): 16 x 32 heads over 33 blocks (226 MB) take 56 us, 4.0 TB/s, 0.62 of a
-// plain copy's rate; compressed records take about four times as many.  For few rows the
-// latency of one item: 8 kv heads x 4 rows over 512 tokens take 6.7 us.
+// Bound: latencies.  16 x 32 heads over 33 blocks of 3 bits (226 MB) take 56 us, 4.0 TB/s,
+// 0.62 of a plain copy's rate, with issue slots 55 %, DRAM 53 % and the tensor pipe 33 % busy:
+// an item is 1690 instructions of a warp in a row, between which it waits for its one stage
+// (K, then V) and for its own products, and sixteen warps per SM do not cover that.
+// Compressed records take about four times the instructions.  For few rows it is the latency
+// of one item: 8 kv heads x 4 rows over 512 tokens take 6.8 us.
 // A kernel with one CTA per record, its codes unpacked for the 5th-generation tensor cores,
 // was slower in both: every item became a chain of barriers, products and tensor-memory
 // reads (114 and 9.8 us).
@@ -292,7 +294,7 @@ __device__ __forceinline__ void tail_scores32(const uint16_t* tail, const uint16
 // infinity or NaN among the values the tokens are added one by one, those of zero weight
 // (masked ones) left out, so that it does not spread.
 // (On the CUDA cores, a token or four channels per lane, 16 x 32 heads over 1024 tokens with
-// a tail of 118 took 39.0 us, this way 29.7.)
+// a tail of 118 took 39.0 us, this way 29.2.)
 template <int G>
 __device__ __forceinline__ void tail_values32(const uint16_t* tail, const float* sc, int n, float* sacc, int lane) {
   const int g = lane >> 2, t = lane & 3;
@@ -407,8 +409,9 @@ struct WinMem {
 };
 
 // Resident CTAs per SM the register budget of the even split is sized for.  Single rows, 16 x
-// 32 heads over 4096 tokens: four CTAs 61.1 / 64.3 / 47.4 us (4 / 3 / 2 bits), five (96
-// registers, a few of them spilled for 3 bits) 63.1 / 65.7 / 45.8, six 69 for 3 bits.
+// 32 heads, the last 4096 of 4500 tokens: four CTAs 56.7 / 59.3 / 44.3 us (4 / 3 / 2 bits),
+// five (96 registers, some spilled) 61.7 / 65.6 / 45.8, six 69 / 72 / 54.  2 bits took five
+// when four took 47.4, before the tail's pieces went to the tensor cores.
 constexpr int win_ctas(int bits, int g, bool even) { return !even ? 0 : (g == 1 ? (bits == 2 ? 5 : 4) : (g == 2 ? 4 : 3)); }
 
 template <int BITS, int G, bool kEven, class Plan>
@@ -944,9 +947,12 @@ long items_per_head(const WindowArgs& a, const Plan* plan, int* most) {
 //   32 kv heads x 2 rows, 18 blocks:      C2 8.6  C1 10.6 E2 11.5          (21 31 22)
 //   2 x 32 kv heads x 4 rows, 18 blocks:  E2 15.1 E4 15.5 C2 16.1  C4 16.8 (35 30 52 42)
 //   16 x 8 kv heads x 4 rows, 33 blocks:  E2 28.7 E4 29.7 C4 32.7  E1 40.6 (124 87 102 210)
-// so: single rows while they give every scheduler of the device at most one item, pairs
+// so, for uncompressed records: single rows while they give every scheduler of the device at most one item, pairs
 // while they fill at most half of the warps it holds, both in clusters; else four rows (or
-// what there is), in clusters while those items fill at most half of the warps.
+// what there is), in clusters while those items fill at most half of the warps.  The host does
+// not know which records are compressed (index entries are on the device), so caches of
+// compressed ones follow the same rule and lose where the brackets differ: 30 against 24 us in
+// the second line, 36 against 28 in the third.
 template <class Plan>
 cudaError_t launch_window_p(WindowArgs a, Plan& plan, cudaStream_t stream) {
   const long per_head = items_per_head(a, &plan, &a.most_items);

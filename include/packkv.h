@@ -295,7 +295,10 @@ packkv_status packkv_attention_decode(const packkv_cache* cache, const uint16_t*
 /* How the frequencies f_i = theta^(-2i/rot_dim) are scaled for contexts longer than the
  * trained ones: LINEAR f/factor; BASE theta * factor^(rot_dim/(rot_dim-2)) in theta's
  * place (rot_dim > 2); PARTS k f + (1-k) f/factor with k = clamp((n - low)/(high - low), 0, 1)
- * and n = original_tokens * f / 2pi, the turns a pair makes within the trained length. */
+ * and n = original_tokens * f / 2pi, the turns a pair makes within the trained length.  The
+ * ramp is linear in the turns (low and high are turns, typically 1 and 32, or 1 and 4).  A
+ * ramp over the pair's number between two rounded borders, or a factor per pair, is none of
+ * these: fill turn[] (below) with those frequencies instead. */
 #define PACKKV_ROPE_SCALE_NONE 0
 #define PACKKV_ROPE_SCALE_LINEAR 1
 #define PACKKV_ROPE_SCALE_BASE 2
